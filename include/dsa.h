@@ -29,7 +29,9 @@
  *     its own workspace; the library's host-side caches and launch counters
  *     are atomic. The profiling hook dsa_profile_events is the exception.
  *   - Layout: row-major, innermost dimension last. bf16 tensors are passed as
- *     raw 16-bit patterns. Every base pointer must be 16-byte aligned.
+ *     raw 16-bit patterns. Every base pointer must be 16-byte aligned (32-bit
+ *     arrays of dsa_plan_step, dsa_norm_rope, dsa_kv_write and dsa_kv_read 4-byte
+ *     aligned where nothing else is said).
  *   - Dimensions: the kernels are built for 64 query heads, latent width 512,
  *     16 index heads of width 128, blocks of 8. Other values of those fields
  *     return DSA_ERR_UNSUPPORTED. k_blocks (1..4096), k_tokens (1..512),
@@ -44,7 +46,8 @@
  *     atomics; every reduction has a fixed order).
  *   - Tracing: each call marks its phases as NVTX ranges (dsa.decode_step,
  *     dsa.decode_multi, dsa.prefill, dsa.compress_append, dsa.pool, dsa.block_stage,
- *     dsa.token_stage, dsa.attention) that a profiler shows on its timeline;
+ *     dsa.token_stage, dsa.attention, dsa.plan, dsa.norm_rope, dsa.kv_write,
+ *     dsa.kv_read) that a profiler shows on its timeline;
  *     with no tool attached a range costs two calls into empty stubs.
  */
 #ifndef DSA_H_
@@ -109,10 +112,20 @@ typedef struct {
  * return DSA_ERR_UNSUPPORTED for them. The attention converts each code to f16
  * exactly and takes the query to f16 with a power-of-two scale per head (exact
  * unless an element is below 2^-24 of its head's largest), so its MMAs run on
- * f16 operands; the probabilities are f16 too (bf16 with bf16 rows). */
+ * f16 operands; the probabilities are f16 too (bf16 with bf16 rows).
+ * Latents "trained to be stored in FP4" (miles.radixark.com "DeepSeek-V4.1
+ * Flash") are read as OCP MXFP4, the format of the 4-bit index keys. 4-bit
+ * rows are taken by the calls above and by dsa_compress_append; prefill and
+ * multi-query calls return DSA_ERR_UNSUPPORTED (dsa_kv_read gives a sequence's
+ * rows back as the bf16 rows they take). The attention converts codes times
+ * scale to bf16 exactly (scale bytes up to 252; 255 stands for NaN).
+ * dsa_kv_write puts rows into a cache of any of the formats. */
 typedef enum {
-  DSA_KV_BF16 = 0,     /* bf16 rows of 512: 1024 bytes a row */
-  DSA_KV_FP8_E4M3 = 1  /* E4M3 codes, 512 bytes a row, standing for code * kv_scale */
+  DSA_KV_BF16 = 0,      /* bf16 rows of 512: 1024 bytes a row */
+  DSA_KV_FP8_E4M3 = 1,  /* E4M3 codes, 512 bytes a row, standing for code * kv_scale */
+  DSA_KV_MXFP4 = 3      /* 272 bytes a row: 256 of e2m1 codes two a byte (element 2i in the
+                           low nibble of byte i), then 16 UE8M0 bytes, byte g the scale
+                           2^(s-127) of elements 32 g .. 32 g + 31; kv_scale not used */
 } dsa_kv_fmt_t;
 
 /*
@@ -125,8 +138,8 @@ typedef enum {
  * with R = page_rows for index keys and latents and R = page_rows / 8 for
  * block keys (a page of page_rows tokens holds page_rows / 8 blocks). So the
  * pools are laid out as [n_pages * R] rows of the cache's own row format
- * (latents: 512 bf16, or 512 E4M3 codes with an fp8 KV cache; keys: their dsa_fmt_t
- * row, MX scales [n_pages * R, 4]).
+ * (latents: the row of cfg->kv_fmt; keys: their dsa_fmt_t row, MX scales
+ * [n_pages * R, 4]).
  *   page_table:    device int32 [B, pages_per_seq]; an entry outside
  *                  [0, n_pages) is a device-detected error (DSA_ERR_DEVICE_CHECK,
  *                  the rows of that page are skipped)
@@ -245,11 +258,14 @@ dsa_status_t dsa_topk(const dsa_config_t* cfg, const void* q_idx, const float* w
  *     lse[b][h] = log sum_j exp(z_j)   (natural log; -inf when there are no rows).
  *   q:        device bf16 [B, 64, 512]
  *   latents:  device bf16, sequence b's row r at (b * latent_seq_stride_rows + r) * 512
- *             (cfg->kv_fmt DSA_KV_FP8_E4M3: uint8 E4M3 codes, the same row layout)
+ *             (cfg->kv_fmt DSA_KV_FP8_E4M3: uint8 E4M3 codes, the same row layout;
+ *             DSA_KV_MXFP4: 272-byte rows, row r at (b * latent_seq_stride_rows + r) * 272)
  *   n_latents: device int32 [B]; an id >= n_latents[b] is flagged and skipped
  *   token_ids: device int32 [B, k_tokens], -1 entries are skipped
  *   swa:      device bf16 [B, window, 512]; slot s holds position T - swa_len[b] + s
- *             (DSA_KV_FP8_E4M3: uint8 E4M3 codes [B, window, 512])
+ *             (DSA_KV_FP8_E4M3: uint8 E4M3 codes [B, window, 512]; DSA_KV_MXFP4: uint8
+ *             [B, window, 272]). The rows' order does not matter to the result, so a
+ *             sequence's slots may also be a ring (position p in slot p % window).
  *   swa_len:  device int32 [B], each in [0, window]
  *   out:      out, device bf16 [B, 64, 512]
  *   lse:      out (optional), device fp32 [B, 64]
@@ -264,9 +280,8 @@ dsa_status_t dsa_sparse_attn_decode(const dsa_config_t* cfg, const void* q, cons
 /*
  * dsa_sparse_attn_decode over a paged latent pool: latent id t of sequence b
  * is row page_table[b * pages_per_seq + t / page_rows] * page_rows + t % page_rows
- * of `latents` (bf16 [pages->n_pages * page_rows, 512], or E4M3 codes with an fp8 KV
- * cache). Ids whose page entry
- * is out of range are skipped and reported like ids past n_latents.
+ * of `latents` (bf16 [pages->n_pages * page_rows, 512], or rows of the other cache
+ * formats). Ids whose page entry is out of range are skipped and reported like ids past n_latents.
  */
 dsa_status_t dsa_sparse_attn_decode_paged(const dsa_config_t* cfg, const void* q,
                                           const void* latents, const dsa_pages_t* pages,
@@ -326,7 +341,8 @@ dsa_status_t dsa_sparse_attn_prefill(const dsa_config_t* cfg, int n_q, int64_t c
  * latents "pooled by a learned softmax gate", one latent per ratio positions).
  * For each sequence b whose token count T_b = n_tokens[b] completes a latent
  * (T_b % ratio == 0), latent j = T_b / ratio - 1 becomes
- *     RN_bf16( sum_i softmax(gate[b])_i * kv[b][i] ),   i = 0 .. ratio - 1
+ *     RN( sum_i softmax(gate[b])_i * kv[b][i] ),   i = 0 .. ratio - 1,
+ * rounded once from fp32 to bf16, or with cfg->kv_fmt DSA_KV_MXFP4 to that format
  * (softmax over the group's ratio logits, in fp32), its index key row becomes
  * new_keys' row b, and the block key of the block holding j is re-pooled as
  * dsa_pool_index_keys(tail_only) does. Sequences that complete no latent are
@@ -337,8 +353,8 @@ dsa_status_t dsa_sparse_attn_prefill(const dsa_config_t* cfg, int n_q, int64_t c
  *   gate:      device fp32 [B, ratio]
  *   new_keys:  the new index key of each sequence, one row per sequence (data
  *              [B, row], MX scales [B, 4]; seq_stride_rows not used)
- *   latents:   bf16, contiguous with latent_seq_stride_rows rows a sequence, or
- *              paged by keys->pages like the keys
+ *   latents:   rows of cfg->kv_fmt (bf16 or MXFP4), contiguous with
+ *              latent_seq_stride_rows rows a sequence, or paged by keys->pages like the keys
  *   keys, pooled: the index-key and block-key caches (written)
  *   max_latents: the caches' capacity; a latent at or past it is a device check
  * ratio must be at most 32 (DSA_ERR_UNSUPPORTED otherwise). The workspace is
@@ -420,13 +436,161 @@ dsa_status_t dsa_topk_noalloc(const dsa_config_t* cfg, const void* q_idx, const 
                               const int32_t* n_latents, int B, int64_t max_latents,
                               int32_t* token_ids, dsa_stream_t stream);
 
+/*
+ * Around the attention of a serving step: the step's plan, the queries and
+ * keys it takes, and the cache rows it reads. A decode loop calls
+ *     dsa_plan_step -> dsa_norm_rope -> dsa_compress_append and dsa_kv_write
+ *     -> dsa_decode_step
+ * on one stream, all from device memory, and captures into a CUDA graph.
+ */
+
+/* A pool of pages that requests share, and its free pages. */
+typedef struct {
+  int32_t* page_table;       /* device [B, pages_per_seq], updated in place */
+  int32_t page_rows;         /* latents per page, a positive multiple of 64 */
+  int32_t pages_per_seq;     /* row stride of page_table */
+  int64_t n_pages;           /* n_pages * page_rows < 2^31 */
+  int32_t* free_ring;        /* device [n_pages]: free pages at positions head .. tail - 1,
+                                modulo n_pages; updated in place */
+  const int64_t* ring_state; /* device {head, tail}, 0 <= tail - head <= n_pages */
+  int64_t* ring_state_out;   /* {head, tail} after the step; may be ring_state itself */
+} dsa_page_pool_t;
+
+/* What a step's plan writes (device arrays; n_tokens may be the input lengths
+ * themselves, no others may overlap). Token arrays hold max_new entries, the
+ * new tokens of request 0 first; entries past the last token hold position 0
+ * and -1 elsewhere. */
+typedef struct {
+  int32_t* n_tokens;     /* [B] lengths after the step */
+  int32_t* n_latents;    /* [B] n_tokens / ratio */
+  int32_t* swa_len;      /* [B] min(n_tokens, window) */
+  int32_t* cu_new;       /* [B + 1] index of each request's first new token; the total last */
+  int32_t* token_seq;    /* [max_new] request of each token */
+  int32_t* positions;    /* [max_new] its position */
+  int32_t* latent_slots; /* [max_new] pool row of the latent it completes, or -1 */
+  int32_t* window_slots; /* [max_new] request * window + position % window for the request's
+                            last `window` positions, -1 for earlier ones */
+  int32_t max_new;       /* 0 .. 2^30; the arrays above are 16-byte aligned */
+} dsa_step_plan_t;
+
+#define DSA_PLAN_MAX_REQUESTS 4096
+
+/*
+ * Block tables and slot maps of a step, built on the GPU from the requests'
+ * lengths (the pages keep caches in pages of a shared pool; how pages are
+ * given out is this library's choice).
+ *   n_tokens: device int32 [B], lengths before the step
+ *   n_new:    device int32 [B], tokens that the step adds to each request (0 is
+ *             fine); a negative number ends the request: its length becomes 0
+ *             and its pages go back to the ring (its table entries are left as
+ *             they are and mean nothing any more)
+ * A request of n tokens holds ceil((n / ratio) / page_rows) pages, entries 0 ..
+ * of its table row. New pages are popped from the ring in request order, then
+ * page order, and ended requests' pages pushed in the same order; a page freed
+ * in a step is not given out in the same step.
+ * All or nothing: when lengths or additions are impossible (negative lengths, more
+ * latents than pages_per_seq pages hold, more new tokens than max_new), the
+ * free pages are too few or the ring's counters are not those of a ring, the
+ * call changes no length, no table entry and nothing of the ring, cu_new is 0,
+ * every token entry is that of a row past the last token, and
+ * dsa_read_device_status reports DSA_ERR_DEVICE_CHECK. A table entry outside
+ * the pool gives -1 slots and is reported, too.
+ * B is at most DSA_PLAN_MAX_REQUESTS (DSA_ERR_UNSUPPORTED above). The workspace
+ * may be of any size that dsa_workspace_size gives.
+ */
+dsa_status_t dsa_plan_step(const dsa_config_t* cfg, int B, const int32_t* n_tokens,
+                           const int32_t* n_new, const dsa_page_pool_t* pool,
+                           const dsa_step_plan_t* plan, void* workspace, size_t workspace_bytes,
+                           dsa_stream_t stream);
+
+/* Element type of the heads of dsa_norm_rope. */
+typedef enum { DSA_DT_BF16 = 0, DSA_DT_F16 = 1, DSA_DT_F32 = 2 } dsa_dtype_t;
+
+/* A group of heads: token t's head h has elements x[t * x_token_stride + h *
+ * x_head_stride + 0 .. dim - 1], and goes to out by out's strides. Strides count
+ * elements and, like the base pointers, are multiples of 16 bytes. out may be
+ * x with the same strides (in place); they must not overlap otherwise. */
+typedef struct {
+  const void* x;
+  void* out;
+  int heads;                 /* >= 0 */
+  int dim;                   /* elements of a head: a multiple of 8, 8 .. 1024 */
+  int64_t x_token_stride, x_head_stride, out_token_stride, out_head_stride;
+  const float* weight;       /* device fp32 [dim], 16-byte aligned, or NULL (all 1) */
+  float eps;                 /* >= 0, finite */
+  int norm;                  /* 0: no norm (weight and eps are not used) */
+  int rope_start;            /* first rotated element, a multiple of 8; < 0: no rotation */
+} dsa_heads_t;
+
+#define DSA_MAX_HEAD_GROUPS 8
+
+/* A rotation: pair i of a token at position p turns by p * inv_freq[i]; cosine
+ * and sine are multiplied by `scale` (1 for plain RoPE, YaRN's factor with it). */
+typedef struct {
+  const double* inv_freq;    /* device fp64 [rope_dim / 2], radians per position */
+  int rope_dim;              /* rotated elements: a multiple of 8 (interleaved) or 16, <= 1024 */
+  int interleaved;           /* pair i: elements 2i and 2i + 1; else i and i + rope_dim / 2 */
+  float scale;
+} dsa_rope_t;
+
+/*
+ * Norms of queries and keys for each head, with the position rotation in the
+ * same pass, over n_groups groups of heads in one launch (the step's queries,
+ * latents, index queries and index keys, for instance):
+ *     y = x / sqrt(mean(x^2) + eps) * weight   over each head's dim elements,
+ *     then elements rope_start .. rope_start + rope_dim - 1 turned in pairs:
+ *     (y0, y1) -> (y0 c - y1 s, y0 s + y1 c).
+ * The pages name a KV norm and RoPE (theta 160000, YaRN x16) and give no
+ * formula; RMS norm and both pairings are the common forms. Arithmetic in fp32
+ * (angles in fp64), one rounding to the elements' type.
+ *   positions: device int32 [n]
+ *   n_valid:   device int32 or NULL: only tokens below *n_valid are done, the
+ *              rows behind them are left as they were (cu_new + B of a plan)
+ *   groups:    host array of n_groups <= DSA_MAX_HEAD_GROUPS
+ *   rope:      NULL: norms only
+ */
+dsa_status_t dsa_norm_rope(int n, const int32_t* n_valid, const int32_t* positions,
+                           dsa_dtype_t dtype, const dsa_heads_t* groups, int n_groups,
+                           const dsa_rope_t* rope, dsa_stream_t stream);
+
+/*
+ * Rows into a cache: bf16 row r of `rows` (r * row_stride elements from its
+ * start) becomes row slots[r] of `cache` in cfg->kv_fmt.
+ *   DSA_KV_BF16: as it is. DSA_KV_FP8_E4M3: RN_e4m3(x / kv_scale, divided in fp32),
+ *   saturating.
+ *   DSA_KV_MXFP4: the OCP MX conversion (scale 2^X, X = floor(log2 amax) - 2 per
+ *   32 elements, at least -127; 2^0 for zeros; elements to nearest, ties to the
+ *   even code, at most 6); a group that holds a NaN or an infinity gets the NaN
+ *   scale.
+ * A negative slot skips its row. The other slots are distinct (of two rows with
+ * one slot, either's bytes may stay). A slot >= n_rows is skipped and reported
+ * (DSA_ERR_DEVICE_CHECK).
+ *   n_valid: as in dsa_norm_rope
+ *   slots:   device int32 [n] (a plan's latent_slots or window_slots)
+ *   cache:   n_rows rows of the format (n_pages * page_rows for a pool,
+ *            B * window for the window rows); n_rows < 2^31
+ */
+dsa_status_t dsa_kv_write(const dsa_config_t* cfg, int n, const int32_t* n_valid, const void* rows,
+                          int64_t row_stride, const int32_t* slots, void* cache, int64_t n_rows,
+                          void* workspace, size_t workspace_bytes, dsa_stream_t stream);
+
+/*
+ * Rows out of a cache: row slots[r] of `cache` as bf16 to row r of `rows`, code
+ * times scale (exact for MXFP4 scales up to 2^125; rounded once for E4M3). Rows
+ * with a negative slot are left as they were. A cache of any format so serves
+ * the calls that read bf16 rows (a sequence's latents for dsa_sparse_attn_prefill).
+ */
+dsa_status_t dsa_kv_read(const dsa_config_t* cfg, int n, const int32_t* n_valid, const void* cache,
+                         int64_t n_rows, const int32_t* slots, void* rows, int64_t row_stride,
+                         void* workspace, size_t workspace_bytes, dsa_stream_t stream);
+
 /* Kernel kinds, for the timing hook and the launch counters below. */
 typedef enum {
   DSA_KERNEL_POOL = 0,    /* block-key pooling */
   DSA_KERNEL_SCAN = 1,    /* indexer scores (block stage and token stage) */
   DSA_KERNEL_SELECT = 2,  /* top-k selection */
   DSA_KERNEL_ATTN = 3,    /* attention */
-  DSA_KERNEL_OTHER = 4,   /* small helpers (identity block lists) */
+  DSA_KERNEL_OTHER = 4,   /* identity block lists, step plans, norms, cache rows */
   DSA_KERNEL_KINDS = 5
 } dsa_kernel_kind_t;
 
@@ -452,7 +616,8 @@ dsa_status_t dsa_launch_counts(uint64_t* counts, int reset);
  * DSA_OK, DSA_ERR_DEVICE_CHECK or DSA_ERR_TIMEOUT (the earliest recorded).
  * If info is not NULL it receives the recorded detail word (0 if none): bits
  * 24..31 name the kernel (1 block-key pooling, 2 indexer scan, 3 top-k
- * selection, 4 attention, 5 prefill partial block, 6 the self-test below),
+ * selection, 4 attention, 5 prefill partial block, 6 the self-test below, 7 step
+ * plan, 8 cache rows),
  * bits 0..23 a detail (for
  * DSA_ERR_TIMEOUT the shared-memory address of the barrier waited on; for
  * DSA_ERR_DEVICE_CHECK the offending sequence index or id).

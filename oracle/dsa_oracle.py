@@ -5,8 +5,7 @@ computes. Only the tests, the smoke check and the benchmark's CPU-baseline leg
 use it; the library never imports it and it imports nothing from the library.
 Floating point runs in float64 except where the method itself fixes a storage
 format (bf16, fp32, e4m3/UE8M0, e2m1/UE8M0); library matmuls serve as plain dot
-products. The MXFP4 index-key format (e2m1 codes) is stated here ahead of the
-library, which does not take it yet.
+products.
 
 The method (DeepSeek-V4.1, two-tier sparse attention):
   * recipes.vllm.ai "DeepSeek-V4.1-Flash", Overview, bullet "Two-tier sparse
@@ -443,7 +442,39 @@ def latent_values(rows: np.ndarray, kv_fmt: str = "bf16", kv_scale: float = 1.0)
         return bf16_to_f64(rows)
     if kv_fmt == "fp8":
         return E4M3_TABLE[np.asarray(rows, np.uint8)] * float(kv_scale)
+    if kv_fmt == "mxfp4":
+        rows = np.asarray(rows, np.uint8)
+        return mxfp4_decode(rows[..., :256], rows[..., 256:])
     raise ValueError(kv_fmt)
+
+
+def latent_rows_mxfp4(v32: np.ndarray) -> np.ndarray:
+    """fp32 rows [..., 512] as 4-bit cache rows (272 bytes: codes, then scales)."""
+    codes, scales = mxfp4_encode(np.asarray(v32, np.float32))
+    return np.concatenate([codes, scales], axis=-1)
+
+
+def norm_rope(x: np.ndarray, weight, eps: float, positions, inv_freq, rope_start: int,
+              interleaved: bool, scale: float = 1.0, norm: bool = True) -> np.ndarray:
+    """RMS norm of each head (last axis) of x [n, heads, dim] times weight, then
+    pairs of the elements from rope_start on turned by position * inv_freq, in
+    float64; rope_start < 0: norm only."""
+    y = np.array(x, np.float64)
+    if norm:
+        y /= np.sqrt((y ** 2).mean(axis=-1, keepdims=True) + eps)
+        if weight is not None:
+            y *= np.asarray(weight, np.float64)
+    if rope_start < 0:
+        return y
+    half = len(inv_freq)
+    a = np.asarray(positions, np.float64)[:, None, None] * np.asarray(inv_freq, np.float64)
+    c, s = scale * np.cos(a), scale * np.sin(a)
+    i = np.arange(half)
+    i0, i1 = (rope_start + 2 * i, rope_start + 2 * i + 1) if interleaved else \
+        (rope_start + i, rope_start + half + i)
+    y0, y1 = y[..., i0], y[..., i1]
+    y[..., i0], y[..., i1] = y0 * c - y1 * s, y0 * s + y1 * c
+    return y
 
 
 def attend_query(cfg: StepConfig, q_bits, latents_bits: np.ndarray, token_ids: np.ndarray,

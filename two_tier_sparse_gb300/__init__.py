@@ -34,7 +34,8 @@ EXPORTS = ("dsa_default_config", "dsa_status_string", "dsa_workspace_size",
            "dsa_decode_step", "dsa_sparse_attn_prefill", "dsa_read_device_status",
            "dsa_profile_events", "dsa_launch_counts", "dsa_topk_noalloc",
            "dsa_selftest_timeout", "dsa_sparse_attn_decode_paged", "dsa_decode_multi",
-           "dsa_compress_append")
+           "dsa_compress_append", "dsa_plan_step", "dsa_norm_rope", "dsa_kv_write",
+           "dsa_kv_read")
 
 TOPK_NOALLOC_MAX_SCORES = 1 << 21
 
@@ -56,7 +57,8 @@ class Config(ctypes.Structure):
                 ("kv_fmt", ctypes.c_int), ("kv_scale", ctypes.c_float)]
 
 
-KV_BF16, KV_FP8_E4M3 = 0, 1
+KV_BF16, KV_FP8_E4M3, KV_MXFP4 = 0, 1, 3
+KV_MXFP4_ROW = 272  # bytes of a 4-bit row: 256 of codes, 16 scales
 
 
 class _Pages(ctypes.Structure):
@@ -69,6 +71,36 @@ class _Keys(ctypes.Structure):
     """dsa_keys_t / dsa_keys_out_t (same layout)."""
     _fields_ = [("fmt", ctypes.c_int), ("data", ctypes.c_void_p), ("scales", ctypes.c_void_p),
                 ("seq_stride_rows", ctypes.c_int64), ("pages", ctypes.POINTER(_Pages))]
+
+
+class _PagePool(ctypes.Structure):
+    """dsa_page_pool_t."""
+    _fields_ = [("page_table", ctypes.c_void_p), ("page_rows", ctypes.c_int32),
+                ("pages_per_seq", ctypes.c_int32), ("n_pages", ctypes.c_int64),
+                ("free_ring", ctypes.c_void_p), ("ring_state", ctypes.c_void_p),
+                ("ring_state_out", ctypes.c_void_p)]
+
+
+class _StepPlan(ctypes.Structure):
+    """dsa_step_plan_t."""
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("n_tokens", "n_latents", "swa_len", "cu_new", "token_seq", "positions",
+                 "latent_slots", "window_slots")] + [("max_new", ctypes.c_int32)]
+
+
+class _HeadsC(ctypes.Structure):
+    """dsa_heads_t."""
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("heads", ctypes.c_int),
+                ("dim", ctypes.c_int), ("x_token_stride", ctypes.c_int64),
+                ("x_head_stride", ctypes.c_int64), ("out_token_stride", ctypes.c_int64),
+                ("out_head_stride", ctypes.c_int64), ("weight", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("norm", ctypes.c_int), ("rope_start", ctypes.c_int)]
+
+
+class _RopeC(ctypes.Structure):
+    """dsa_rope_t."""
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rope_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
 _lib = None
@@ -110,6 +142,12 @@ def load() -> ctypes.CDLL:
                                          vp, vp, vp, vp, sz, vp]
         lib.dsa_compress_append.argtypes = [cp, i32, vp, vp, vp, kp, vp, i64, kp, kp, i64, vp,
                                             sz, vp]
+        lib.dsa_plan_step.argtypes = [cp, i32, vp, vp, ctypes.POINTER(_PagePool),
+                                      ctypes.POINTER(_StepPlan), vp, sz, vp]
+        lib.dsa_norm_rope.argtypes = [i32, vp, vp, i32, ctypes.POINTER(_HeadsC), i32,
+                                      ctypes.POINTER(_RopeC), vp]
+        lib.dsa_kv_write.argtypes = [cp, i32, vp, vp, i64, vp, vp, i64, vp, sz, vp]
+        lib.dsa_kv_read.argtypes = [cp, i32, vp, vp, i64, vp, vp, i64, vp, sz, vp]
         for f in EXPORTS:
             if f not in ("dsa_default_config", "dsa_status_string"):
                 getattr(lib, f).restype = ctypes.c_int
@@ -135,8 +173,10 @@ def _stream(stream=None):
 
 def config(k_blocks=2048, k_tokens=512, window=128, ratio=1, sm_scale=0.0, kv_fmt=KV_BF16,
            kv_scale=1.0) -> Config:
-    """kv_fmt: KV_BF16, or KV_FP8_E4M3 (latents and window rows as E4M3 codes
-    standing for code * kv_scale; decode attention and the decode step only)."""
+    """kv_fmt: KV_BF16, KV_FP8_E4M3 (latents and window rows as E4M3 codes standing
+    for code * kv_scale; decode attention and the decode step only) or KV_MXFP4
+    (272-byte rows of e2m1 codes and their scales; the same calls and
+    compress_append)."""
     c = Config()
     load().dsa_default_config(ctypes.byref(c))
     c.k_blocks, c.k_tokens, c.window, c.ratio = k_blocks, k_tokens, window, ratio
@@ -288,6 +328,232 @@ def sparse_attn_prefill(cfg, ctx_len, q, q_idx, w, latents, keys: Keys, pooled: 
                                           ctypes.byref(pooled.c()), _p(swa), _p(out), _p(lse),
                                           _p(token_ids), _p(ws), ws.numel(), _stream(stream)),
            "dsa_sparse_attn_prefill")
+
+
+def _launch_stream(t: torch.Tensor, stream):
+    """The raw stream to launch on: the given one, or the current stream of t's
+    device, which has to be the current device (the library launches there)."""
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"tensors on device {dev}, but the current device is "
+                         f"{torch.cuda.current_device()}")
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _i32(name, t, shape=None, optional=False):
+    if t is None and optional:
+        return
+    if t.dtype != torch.int32 or not t.is_contiguous() or (shape is not None
+                                                           and tuple(t.shape) != shape):
+        raise ValueError(f"{name}: a contiguous int32 tensor"
+                         + (f" of shape {list(shape)}" if shape is not None else "")
+                         + f", not {t.dtype} {list(t.shape)}")
+
+
+class PagePool:
+    """A pool of pages and its free pages (dsa_page_pool_t): table int32
+    [B, pages_per_seq], free_ring int32 [n_pages] with the free pages at positions
+    head .. tail - 1 modulo n_pages, ring_state int64 {head, tail}. All are updated
+    by plan_step; ring_state_out keeps ring_state as it is and takes its place."""
+
+    def __init__(self, table: torch.Tensor, page_rows: int, free_ring: torch.Tensor,
+                 ring_state: torch.Tensor, ring_state_out: Optional[torch.Tensor] = None):
+        _i32("table", table)
+        _i32("free_ring", free_ring)
+        out = ring_state if ring_state_out is None else ring_state_out
+        if table.dim() != 2 or free_ring.dim() != 1:
+            raise ValueError("table has two dimensions and free_ring one")
+        for r in (ring_state, out):
+            if r.dtype != torch.int64 or r.numel() != 2 or not r.is_contiguous():
+                raise ValueError("ring_state: two int64 values")
+        self.table, self.page_rows, self.free_ring = table, page_rows, free_ring
+        self.ring_state, self.ring_state_out = ring_state, out
+        self.c = _PagePool(table.data_ptr(), page_rows, table.shape[1], free_ring.shape[0],
+                           free_ring.data_ptr(), ring_state.data_ptr(), out.data_ptr())
+        self._ref = ctypes.byref(self.c)
+
+    @classmethod
+    def empty(cls, B: int, page_rows: int, pages_per_seq: int, n_pages: int, device="cuda"):
+        """A pool with every page free and no request holding any."""
+        return cls(torch.full((B, pages_per_seq), -1, dtype=torch.int32, device=device), page_rows,
+                   torch.arange(n_pages, dtype=torch.int32, device=device),
+                   torch.tensor([0, n_pages], dtype=torch.int64, device=device))
+
+    def pages(self) -> Pages:
+        """The pool's page table as the caches' calls take it."""
+        return Pages(self.table, self.page_rows, self.free_ring.shape[0])
+
+
+class StepPlan:
+    """What plan_step writes (dsa_step_plan_t), int32 tensors: n_tokens, n_latents and
+    swa_len [B], cu_new [B + 1], and per new token (max_new entries) token_seq,
+    positions, latent_slots and window_slots. n_tokens may be the input lengths."""
+
+    def __init__(self, n_tokens, n_latents, swa_len, cu_new, token_seq, positions, latent_slots,
+                 window_slots):
+        B, m = n_tokens.shape[0], token_seq.shape[0]
+        for name, t, n in (("n_tokens", n_tokens, B), ("n_latents", n_latents, B),
+                           ("swa_len", swa_len, B), ("cu_new", cu_new, B + 1),
+                           ("token_seq", token_seq, m), ("positions", positions, m),
+                           ("latent_slots", latent_slots, m), ("window_slots", window_slots, m)):
+            _i32(name, t, (n,))
+            setattr(self, name, t)
+        self.max_new = m
+        self.c = _StepPlan(n_tokens.data_ptr(), n_latents.data_ptr(), swa_len.data_ptr(),
+                           cu_new.data_ptr(), token_seq.data_ptr(), positions.data_ptr(),
+                           latent_slots.data_ptr(), window_slots.data_ptr(), m)
+        self._ref = ctypes.byref(self.c)
+
+    @classmethod
+    def empty(cls, B: int, max_new: int, device="cuda", n_tokens=None):
+        """Tensors for B requests and up to max_new new tokens a step."""
+        def new(n):
+            return torch.zeros((n,), dtype=torch.int32, device=device)
+        return cls(new(B) if n_tokens is None else n_tokens, new(B), new(B), new(B + 1),
+                   new(max_new), new(max_new), new(max_new), new(max_new))
+
+    @property
+    def n_valid(self) -> torch.Tensor:
+        """The step's number of new tokens, on the device (cu_new's last entry)."""
+        return self.cu_new[-1:]
+
+
+def plan_step(cfg, n_tokens, n_new, pool: PagePool, plan: StepPlan, ws, stream=None):
+    """Block table and slot maps of a step (dsa_plan_step): n_tokens [B] lengths
+    before the step, n_new [B] tokens added (negative: the request ends)."""
+    B = plan.n_tokens.shape[0]
+    if n_tokens.dtype != torch.int32 or n_new.dtype != torch.int32 or n_tokens.shape != (B,) or \
+            n_new.shape != (B,) or pool.table.shape[0] != B or \
+            not (n_tokens.is_contiguous() and n_new.is_contiguous()):
+        raise ValueError(f"n_tokens and n_new: contiguous int32 tensors of the plan's {B} requests, "
+                         f"the pool's table a row for each")
+    code = load().dsa_plan_step(ctypes.byref(cfg), B, n_tokens.data_ptr(), n_new.data_ptr(),
+                                pool._ref, plan._ref, ws.data_ptr(), ws.numel(),
+                                _launch_stream(n_tokens, stream))
+    if code:
+        raise DsaError(code, "dsa_plan_step")
+
+
+_DT = {torch.bfloat16: 0, torch.int16: 0, torch.float16: 1, torch.float32: 2}
+
+
+class Heads:
+    """A group of heads for norm_rope (dsa_heads_t): x [n, heads, dim] or [n, dim]
+    with contiguous elements and any token and head strides (a slice of a fused
+    projection, say), out like x (x itself: in place). weight fp32 [dim] or None;
+    norm=False rotates only; rope_start: first rotated element, None for no rotation."""
+
+    def __init__(self, x: torch.Tensor, out: Optional[torch.Tensor] = None,
+                 weight: Optional[torch.Tensor] = None, eps: float = 1e-6, norm: bool = True,
+                 rope_start: Optional[int] = None):
+        out = x if out is None else out
+        if x.dtype not in _DT or out.dtype not in _DT or _DT[x.dtype] != _DT[out.dtype]:
+            raise ValueError("x and out: bf16 (or its bits in int16), f16 or f32, both alike")
+        if x.dim() not in (2, 3) or out.shape != x.shape or x.stride(-1) != 1 or \
+                out.stride(-1) != 1:
+            raise ValueError("x and out: [n, heads, dim] or [n, dim] with contiguous elements")
+        if weight is not None and (weight.dtype != torch.float32 or not weight.is_contiguous()
+                                   or weight.shape != x.shape[-1:]):
+            raise ValueError("weight: contiguous fp32 [dim]")
+        if any(t is not None and t.get_device() != x.get_device() for t in (out, weight)):
+            raise ValueError("x, out and weight on one device")
+        self.x, self.out, self.weight = x, out, weight
+        self.n, self.dtype = x.shape[0], _DT[x.dtype]
+        heads = x.shape[1] if x.dim() == 3 else 1
+
+        def strides(t):
+            return t.stride(0), t.stride(1) if t.dim() == 3 and heads > 1 else t.shape[-1]
+        self.c = _HeadsC(x.data_ptr(), out.data_ptr(), heads, x.shape[-1], *strides(x),
+                         *strides(out), weight.data_ptr() if weight is not None else None, eps,
+                         int(norm), -1 if rope_start is None else rope_start)
+
+
+class HeadSet:
+    """The groups of heads of one norm_rope call, of one element type and token count."""
+
+    def __init__(self, groups):
+        groups = list(groups)
+        if not groups or any(g.n != groups[0].n or g.dtype != groups[0].dtype or
+                             g.x.get_device() != groups[0].x.get_device() for g in groups):
+            raise ValueError("groups of one element type, token count and device")
+        self.groups = groups
+        self.n, self.dtype = groups[0].n, groups[0].dtype
+        self._c = (_HeadsC * len(groups))(*[g.c for g in groups])
+
+
+class Rope:
+    """A rotation (dsa_rope_t): inv_freq fp64 [rope_dim / 2] on the device, radians per
+    position; interleaved pairs (2i, 2i + 1) or halves (i, i + rope_dim / 2); cosine
+    and sine times scale."""
+
+    def __init__(self, inv_freq: torch.Tensor, interleaved: bool = True, scale: float = 1.0):
+        if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+            raise ValueError("inv_freq: contiguous fp64 [rope_dim / 2]")
+        self.inv_freq = inv_freq
+        self.c = _RopeC(inv_freq.data_ptr(), 2 * inv_freq.shape[0], int(interleaved), scale)
+        self._ref = ctypes.byref(self.c)
+
+
+def norm_rope(positions, heads: HeadSet, rope: Optional[Rope] = None, n_valid=None, stream=None):
+    """Norms of heads and their rotation in one pass (dsa_norm_rope): positions int32
+    [n]; n_valid: device int32 [1], tokens behind it are left as they were."""
+    n = heads.n
+    if rope is not None or positions is not None:
+        if positions is None or positions.dtype != torch.int32 or positions.shape != (n,) or \
+                not positions.is_contiguous():
+            raise ValueError(f"positions: contiguous int32 [{n}]")
+    _i32("n_valid", n_valid, (1,), optional=True)
+    code = load().dsa_norm_rope(n, None if n_valid is None else n_valid.data_ptr(),
+                                None if positions is None else positions.data_ptr(), heads.dtype,
+                                heads._c, len(heads._c), None if rope is None else rope._ref,
+                                _launch_stream(heads.groups[0].x, stream))
+    if code:
+        raise DsaError(code, "dsa_norm_rope")
+
+
+_KV_ROW = {KV_BF16: 1024, KV_FP8_E4M3: 512, KV_MXFP4: KV_MXFP4_ROW}
+
+
+def _rows_call(cfg, rows, slots, cache, n_valid):
+    """Checks what kv_write and kv_read share; returns (n, row stride, cache rows)."""
+    row = _KV_ROW.get(cfg.kv_fmt)
+    if row is None:
+        raise DsaError(1, "kv_fmt")
+    if rows.dtype not in (torch.bfloat16, torch.int16) or rows.dim() != 2 or \
+            rows.shape[1] != 512 or rows.stride(1) != 1:
+        raise ValueError("rows: bf16 (or its bits in int16) [n, 512] with contiguous elements")
+    n = rows.shape[0]
+    _i32("slots", slots, (n,))
+    _i32("n_valid", n_valid, (1,), optional=True)
+    size = cache.numel() * cache.element_size()
+    if not cache.is_contiguous() or cache.shape[-1] * cache.element_size() != row:
+        raise ValueError(f"cache: contiguous rows of {row} bytes")
+    return n, rows.stride(0), size // row
+
+
+def kv_write(cfg, rows, slots, cache, ws, n_valid=None, stream=None):
+    """bf16 rows [n, 512] into a cache of cfg.kv_fmt (dsa_kv_write): row r becomes cache
+    row slots[r], negative slots skip; cache: [..., row] contiguous (a pool of pages, or
+    the window rows)."""
+    n, stride, n_rows = _rows_call(cfg, rows, slots, cache, n_valid)
+    code = load().dsa_kv_write(ctypes.byref(cfg), n,
+                               None if n_valid is None else n_valid.data_ptr(), rows.data_ptr(),
+                               stride, slots.data_ptr(), cache.data_ptr(), n_rows, ws.data_ptr(),
+                               ws.numel(), _launch_stream(rows, stream))
+    if code:
+        raise DsaError(code, "dsa_kv_write")
+
+
+def kv_read(cfg, cache, slots, rows, ws, n_valid=None, stream=None):
+    """Rows slots[r] of a cache back as bf16 rows [n, 512] (dsa_kv_read); rows with a
+    negative slot are left as they were."""
+    n, stride, n_rows = _rows_call(cfg, rows, slots, cache, n_valid)
+    code = load().dsa_kv_read(ctypes.byref(cfg), n,
+                              None if n_valid is None else n_valid.data_ptr(), cache.data_ptr(),
+                              n_rows, slots.data_ptr(), rows.data_ptr(), stride, ws.data_ptr(),
+                              ws.numel(), _launch_stream(rows, stream))
+    if code:
+        raise DsaError(code, "dsa_kv_read")
 
 
 def read_device_status(ws, stream=None):

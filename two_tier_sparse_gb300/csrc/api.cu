@@ -75,7 +75,9 @@ dsa_status_t check_config(const dsa_config_t* c) {
       !(c->sm_scale == c->sm_scale) || isinf(c->sm_scale)) {
     return DSA_ERR_INVALID_ARG;
   }
-  if (c->kv_fmt != DSA_KV_BF16 && c->kv_fmt != DSA_KV_FP8_E4M3) return DSA_ERR_INVALID_ARG;
+  if (c->kv_fmt != DSA_KV_BF16 && c->kv_fmt != DSA_KV_FP8_E4M3 && c->kv_fmt != DSA_KV_MXFP4) {
+    return DSA_ERR_INVALID_ARG;
+  }
   if (c->kv_fmt == DSA_KV_FP8_E4M3 && !(c->kv_scale > 0.f && !isinf(c->kv_scale))) {
     return DSA_ERR_INVALID_ARG;
   }
@@ -220,6 +222,11 @@ cudaError_t launch(int kind, cudaStream_t s, F&& f) {
     return cudaEventRecord(static_cast<cudaEvent_t>(p.ends[slot]), s);
   }
   return cudaSuccess;
+}
+
+// The decode attention over the cache's format.
+cudaError_t launch_decode_attn(const AttnArgs& a, const dsa_config_t& c, cudaStream_t s) {
+  return c.kv_fmt == DSA_KV_MXFP4 ? launch_attn4(a, s) : launch_attn(a, s);
 }
 
 // The workspace's selection scratch, or null when no query can have more than
@@ -638,7 +645,7 @@ dsa_status_t attn_decode(const dsa_config_t* cfg, const void* q, const void* lat
   a.status = at<DeviceStatus>(workspace, L.status);
   set_splits(a, *cfg, B);
   Range range("dsa.attention");
-  DSA_CUDA(launch(DSA_KERNEL_ATTN, static_cast<cudaStream_t>(stream), [&](int*) { return launch_attn(a, static_cast<cudaStream_t>(stream)); }));
+  DSA_CUDA(launch(DSA_KERNEL_ATTN, static_cast<cudaStream_t>(stream), [&](int*) { return launch_decode_attn(a, *cfg, static_cast<cudaStream_t>(stream)); }));
   return DSA_OK;
 }
 
@@ -765,7 +772,7 @@ dsa_status_t dsa_decode_step(const dsa_config_t* cfg, const void* q, const void*
   a.status = st;
   set_splits(a, *cfg, B);
   Range attn_range("dsa.attention");
-  DSA_CUDA(launch(DSA_KERNEL_ATTN, s, [&](int*) { return launch_attn(a, s); }));
+  DSA_CUDA(launch(DSA_KERNEL_ATTN, s, [&](int*) { return launch_decode_attn(a, *cfg, s); }));
   return DSA_OK;
 }
 
@@ -776,7 +783,7 @@ dsa_status_t dsa_sparse_attn_prefill(const dsa_config_t* cfg, int n_q, int64_t c
                                      float* lse, int32_t* token_ids, void* workspace,
                                      size_t workspace_bytes, dsa_stream_t stream) {
   DSA_TRY(check_config(cfg));
-  if (cfg->kv_fmt != DSA_KV_BF16) return DSA_ERR_UNSUPPORTED;  // fp8 caches: decode only
+  if (cfg->kv_fmt != DSA_KV_BF16) return DSA_ERR_UNSUPPORTED;  // fp8 and 4-bit caches: decode only
   if (n_q < 0 || ctx_len < 0) return DSA_ERR_INVALID_ARG;
   const int64_t n_lat = (ctx_len + n_q) / cfg->ratio;
   if (n_lat > kMaxLatents) return DSA_ERR_INVALID_ARG;
@@ -839,7 +846,7 @@ dsa_status_t dsa_decode_multi(const dsa_config_t* cfg, int n_q, const int32_t* n
                               int32_t* token_ids, void* workspace, size_t workspace_bytes,
                               dsa_stream_t stream) {
   DSA_TRY(check_config(cfg));
-  if (cfg->kv_fmt != DSA_KV_BF16) return DSA_ERR_UNSUPPORTED;  // fp8 caches: single-query decode
+  if (cfg->kv_fmt != DSA_KV_BF16) return DSA_ERR_UNSUPPORTED;  // others: single-query decode
   if (n_q < 1 || B < 0 || max_latents < 0 || max_latents > kMaxLatents ||
       latent_seq_stride_rows < max_latents || static_cast<int64_t>(B) * n_q > (1 << 30)) {
     return DSA_ERR_INVALID_ARG;
@@ -907,7 +914,7 @@ dsa_status_t dsa_compress_append(const dsa_config_t* cfg, int B, const int32_t* 
                                  dsa_stream_t stream) {
   DSA_TRY(check_config(cfg));
   if (cfg->ratio > 32) return DSA_ERR_UNSUPPORTED;
-  if (cfg->kv_fmt != DSA_KV_BF16) return DSA_ERR_UNSUPPORTED;  // it writes bf16 latents
+  if (cfg->kv_fmt == DSA_KV_FP8_E4M3) return DSA_ERR_UNSUPPORTED;  // it writes bf16 or MXFP4 latents
   if (B < 0 || max_latents < 0 || max_latents > kMaxLatents || keys == nullptr ||
       pooled == nullptr || new_keys == nullptr) {
     return DSA_ERR_INVALID_ARG;
@@ -946,7 +953,8 @@ dsa_status_t dsa_compress_append(const dsa_config_t* cfg, int B, const int32_t* 
   ap.fmt = keys->fmt;
   ap.new_key = static_cast<const uint8_t*>(new_keys->data);
   ap.new_scales = new_keys->scales;
-  ap.latents = static_cast<uint16_t*>(latents);
+  ap.kv_fmt = cfg->kv_fmt;
+  ap.latents = latents;
   ap.lat_stride = latent_seq_stride_rows;
   ap.key_data = static_cast<uint8_t*>(keys->data);
   ap.key_scales = keys->scales;
@@ -975,6 +983,214 @@ dsa_status_t dsa_compress_append(const dsa_config_t* cfg, int B, const int32_t* 
                           (max_latents + kBlock - 1) / kBlock);
   a.status = st;
   DSA_CUDA(launch(DSA_KERNEL_POOL, s, [&](int*) { return launch_pool(a, s); }));
+  return DSA_OK;
+}
+
+dsa_status_t dsa_plan_step(const dsa_config_t* cfg, int B, const int32_t* n_tokens,
+                           const int32_t* n_new, const dsa_page_pool_t* pool,
+                           const dsa_step_plan_t* plan, void* workspace, size_t workspace_bytes,
+                           dsa_stream_t stream) {
+  DSA_TRY(check_config(cfg));
+  if (B < 0 || pool == nullptr || plan == nullptr ||
+      (B > 0 && (n_tokens == nullptr || n_new == nullptr))) {
+    return DSA_ERR_INVALID_ARG;
+  }
+  if (B > DSA_PLAN_MAX_REQUESTS) return DSA_ERR_UNSUPPORTED;
+  if ((B > 0 && pool->page_table == nullptr) || pool->free_ring == nullptr ||
+      pool->ring_state == nullptr || pool->ring_state_out == nullptr || pool->page_rows <= 0 || pool->page_rows % 64 != 0 ||
+      pool->n_pages < 1 || pool->pages_per_seq < 1 || pool->n_pages >= (int64_t{1} << 31) ||
+      pool->n_pages * pool->page_rows >= (int64_t{1} << 31)) {
+    return DSA_ERR_INVALID_ARG;
+  }
+  if ((B > 0 && (plan->n_tokens == nullptr || plan->n_latents == nullptr ||
+                 plan->swa_len == nullptr)) ||
+      plan->cu_new == nullptr || plan->max_new < 0 || plan->max_new > (1 << 30) ||
+      (plan->max_new > 0 && (plan->token_seq == nullptr || plan->positions == nullptr ||
+                             plan->latent_slots == nullptr || plan->window_slots == nullptr))) {
+    return DSA_ERR_INVALID_ARG;
+  }
+  auto off4 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; };
+  auto off8 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) != 0; };
+  if (off4(n_tokens) || off4(n_new) || off4(pool->page_table) || off4(pool->free_ring) ||
+      off8(pool->ring_state) || off8(pool->ring_state_out) || off4(plan->n_tokens) ||
+      off4(plan->n_latents) || off4(plan->swa_len) || off4(plan->cu_new) ||
+      !aligned16(plan->token_seq) || !aligned16(plan->positions) ||
+      !aligned16(plan->latent_slots) || !aligned16(plan->window_slots)) {
+    return DSA_ERR_MISALIGNED;
+  }
+  // window slots are 32-bit (B * window < 2^20 here)
+  if (workspace == nullptr || workspace_bytes < sizeof(DeviceStatus)) return DSA_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(workspace) % kAlign) return DSA_ERR_MISALIGNED;
+  Range range("dsa.plan");
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  DeviceStatus* st = static_cast<DeviceStatus*>(workspace);
+  PlanArgs a{};
+  a.B = B;
+  a.ratio = cfg->ratio;
+  a.window = cfg->window;
+  a.n_tokens = n_tokens;
+  a.n_new = n_new;
+  a.table = pool->page_table;
+  a.page_rows = pool->page_rows;
+  a.pages_per_seq = pool->pages_per_seq;
+  a.n_pages = pool->n_pages;
+  a.ring = pool->free_ring;
+  a.ring_state = pool->ring_state;
+  a.ring_state_out = pool->ring_state_out;
+  a.n_tokens_out = plan->n_tokens;
+  a.n_latents = plan->n_latents;
+  a.swa_len = plan->swa_len;
+  a.cu_new = plan->cu_new;
+  a.max_new = plan->max_new;
+  a.token_seq = plan->token_seq;
+  a.positions = plan->positions;
+  a.latent_slots = plan->latent_slots;
+  a.window_slots = plan->window_slots;
+  a.ticket = &st->ticket;
+  a.status = st;
+  DSA_CUDA(launch(DSA_KERNEL_OTHER, s, [&](int*) { return launch_plan(a, s); }));
+  return DSA_OK;
+}
+
+dsa_status_t dsa_norm_rope(int n, const int32_t* n_valid, const int32_t* positions,
+                           dsa_dtype_t dtype, const dsa_heads_t* groups, int n_groups,
+                           const dsa_rope_t* rope, dsa_stream_t stream) {
+  if (n < 0 || n_groups < 0 || (n_groups > 0 && groups == nullptr)) return DSA_ERR_INVALID_ARG;
+  if (dtype != DSA_DT_BF16 && dtype != DSA_DT_F16 && dtype != DSA_DT_F32) {
+    return DSA_ERR_INVALID_ARG;
+  }
+  if (n_groups > DSA_MAX_HEAD_GROUPS) return DSA_ERR_UNSUPPORTED;
+  auto off4 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; };
+  NormRopeArgs a{};
+  if (rope != nullptr) {
+    if (rope->inv_freq == nullptr || (n > 0 && positions == nullptr) || rope->rope_dim < 8 ||
+        rope->rope_dim > 1024 || rope->rope_dim % (rope->interleaved ? 8 : 16) != 0 ||
+        !isfinite(rope->scale)) {
+      return DSA_ERR_INVALID_ARG;
+    }
+    if ((reinterpret_cast<uintptr_t>(rope->inv_freq) & 7u) || off4(positions)) {
+      return DSA_ERR_MISALIGNED;
+    }
+    a.inv_freq = rope->inv_freq;
+    a.pairs = rope->rope_dim / 2;
+    a.interleaved = rope->interleaved != 0;
+    a.rope_scale = rope->scale;
+  }
+  if (off4(n_valid)) return DSA_ERR_MISALIGNED;
+  const int64_t elems = dtype == DSA_DT_F32 ? 4 : 8;  // of 16 bytes
+  int max_dim = 0, used = 0;
+  int64_t units = 0;
+  for (int g = 0; g < n_groups; ++g) {
+    const dsa_heads_t& h = groups[g];
+    if (h.heads < 0 || h.dim < 8 || h.dim > 1024 || h.dim % 8 != 0) return DSA_ERR_INVALID_ARG;
+    if (h.norm && !(h.eps >= 0.f && isfinite(h.eps))) return DSA_ERR_INVALID_ARG;
+    if (h.rope_start >= 0 &&
+        (rope == nullptr || h.rope_start % 8 != 0 || h.rope_start + rope->rope_dim > h.dim)) {
+      return DSA_ERR_INVALID_ARG;
+    }
+    if (h.heads == 0 || n == 0) continue;
+    if (h.x == nullptr || h.out == nullptr) return DSA_ERR_INVALID_ARG;
+    if (!aligned16(h.x) || !aligned16(h.out) || (h.norm && h.weight && !aligned16(h.weight)) ||
+        h.x_token_stride % elems || h.x_head_stride % elems || h.out_token_stride % elems ||
+        h.out_head_stride % elems) {
+      return DSA_ERR_MISALIGNED;
+    }
+    if (h.x == h.out &&
+        (h.x_token_stride != h.out_token_stride || h.x_head_stride != h.out_head_stride)) {
+      return DSA_ERR_INVALID_ARG;
+    }
+    NormRopeSeg& sg = a.seg[used++];
+    sg.x = h.x;
+    sg.out = h.out;
+    sg.x_token_stride = h.x_token_stride;
+    sg.x_head_stride = h.x_head_stride;
+    sg.out_token_stride = h.out_token_stride;
+    sg.out_head_stride = h.out_head_stride;
+    sg.weight = h.norm ? h.weight : nullptr;
+    sg.heads = h.heads;
+    sg.dim = h.dim;
+    while ((8 << sg.lanes_log2) < h.dim && sg.lanes_log2 < 5) ++sg.lanes_log2;
+    units += (int64_t{h.heads} + (32 >> sg.lanes_log2) - 1) / (32 >> sg.lanes_log2);
+    if (units > (1 << 24)) return DSA_ERR_UNSUPPORTED;
+    sg.unit_end = static_cast<int>(units);
+    sg.norm = h.norm != 0;
+    sg.rope = h.rope_start >= 0;
+    sg.rope_start = h.rope_start;
+    sg.eps = h.eps;
+    sg.inv_dim = 1.f / static_cast<float>(h.dim);
+    max_dim = std::max(max_dim, h.dim);
+  }
+  if (n == 0 || units == 0) return DSA_OK;
+  a.n = n;
+  a.n_valid = n_valid;
+  a.positions = positions;
+  a.units = static_cast<int>(units);
+  Range range("dsa.norm_rope");
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  DSA_CUDA(launch(DSA_KERNEL_OTHER, s, [&](int*) { return launch_norm_rope(a, dtype, max_dim, s); }));
+  return DSA_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// dsa_kv_write and dsa_kv_read: the checks and the arguments they share.
+dsa_status_t rows_args(const dsa_config_t* cfg, int n, const int32_t* n_valid, const void* rows,
+                       int64_t row_stride, const int32_t* slots, const void* cache, int64_t n_rows,
+                       void* workspace, size_t workspace_bytes, RowsArgs* a) {
+  DSA_TRY(check_config(cfg));
+  if (n < 0 || n_rows < 0 || n_rows >= (int64_t{1} << 31) ||
+      (n > 0 && (rows == nullptr || slots == nullptr || (n_rows > 0 && cache == nullptr)))) {
+    return DSA_ERR_INVALID_ARG;
+  }
+  if (!aligned16(rows) || !aligned16(cache) || row_stride % 8 != 0 ||
+      (reinterpret_cast<uintptr_t>(slots) & 3u) || (reinterpret_cast<uintptr_t>(n_valid) & 3u)) {
+    return DSA_ERR_MISALIGNED;
+  }
+  if (row_stride < kLatent && n > 1) return DSA_ERR_INVALID_ARG;
+  if (workspace == nullptr || workspace_bytes < sizeof(DeviceStatus)) return DSA_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(workspace) % kAlign) return DSA_ERR_MISALIGNED;
+  a->n = n;
+  a->n_valid = n_valid;
+  a->rows = rows;
+  a->row_stride = row_stride;
+  a->slots = slots;
+  a->cache = const_cast<void*>(cache);
+  a->n_rows = n_rows;
+  a->kv_fmt = cfg->kv_fmt;
+  a->kv_scale = cfg->kv_scale;
+  a->status = static_cast<DeviceStatus*>(workspace);
+  return DSA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+dsa_status_t dsa_kv_write(const dsa_config_t* cfg, int n, const int32_t* n_valid, const void* rows,
+                          int64_t row_stride, const int32_t* slots, void* cache, int64_t n_rows,
+                          void* workspace, size_t workspace_bytes, dsa_stream_t stream) {
+  RowsArgs a{};
+  DSA_TRY(rows_args(cfg, n, n_valid, rows, row_stride, slots, cache, n_rows, workspace,
+                    workspace_bytes, &a));
+  if (n == 0) return DSA_OK;
+  Range range("dsa.kv_write");
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  DSA_CUDA(launch(DSA_KERNEL_OTHER, s, [&](int*) { return launch_kv_write(a, s); }));
+  return DSA_OK;
+}
+
+dsa_status_t dsa_kv_read(const dsa_config_t* cfg, int n, const int32_t* n_valid, const void* cache,
+                         int64_t n_rows, const int32_t* slots, void* rows, int64_t row_stride,
+                         void* workspace, size_t workspace_bytes, dsa_stream_t stream) {
+  RowsArgs a{};
+  DSA_TRY(rows_args(cfg, n, n_valid, rows, row_stride, slots, cache, n_rows, workspace,
+                    workspace_bytes, &a));
+  if (n == 0) return DSA_OK;
+  Range range("dsa.kv_read");
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  DSA_CUDA(launch(DSA_KERNEL_OTHER, s, [&](int*) { return launch_kv_read(a, s); }));
   return DSA_OK;
 }
 

@@ -1,0 +1,751 @@
+// S5 - S7 over a cache held in 4 bits (DSA_KV_MXFP4): decode attention of 64
+// heads over the selected latents and the sliding window under one softmax,
+// the rows e2m1 codes with a power-of-two scale per 32 elements.
+//
+//   S   = Q . KV^T    (M = 128 with the 64 heads in lanes 0..63, N = 64 rows, K = 512)
+//   O^T += KV^T . P^T (four M = 128 slices of the 512 latent dims, N = 64 heads,
+//                      K = 64 rows; the KV tile is read as an MN-major operand)
+//
+// A row is 272 bytes, so a CTA's rows fit in registers on their way: eight
+// loader warps read a tile's codes (16 bytes a lane: 32 elements, one scale)
+// while they convert the tile before it to bf16 into a swizzled operand slot.
+// bf16 holds every code times every scale exactly, so Q stays as it is given
+// and the MMAs see the cache's own values. Tiles have 64 rows (two slots of
+// 64 KB): the MMAs here are bound by the operands they read from shared memory
+// (M x K + N x K elements at 128 bytes a clock), which makes a QK^T step over
+// 32 rows cost as much as one over 64; a row's bytes no longer set the pace,
+// so nothing is gained by smaller tiles.
+//
+// The split over a cluster of S CTAs, the lazy softmax maximum and the roles
+// are those of the attention over bf16 rows. The partial outputs that the CTAs
+// of a cluster exchange keep 24 bits of their fp32 value (sign, exponent, 15
+// mantissa bits), as a 16-bit and an 8-bit part: with bf16 parts their rounding
+// would add to the output's own, which is of the same size.
+#include <algorithm>
+#include <cstddef>
+
+#include "attn_math.cuh"
+#include "kv_format.cuh"
+
+namespace dsa {
+
+namespace {
+
+constexpr int kRows = 64;                          // rows of a tile
+constexpr int kSlots = 2;
+constexpr int kLoadWarp0 = 4;
+constexpr int kLoadWarps = 8;
+constexpr int kWarpRows = kRows / kLoadWarps;      // 8 rows of a tile for each loader warp
+constexpr int kMmaWarp = kLoadWarp0 + kLoadWarps;  // 12: QK^T issuer (and TMEM owner)
+constexpr int kPvWarp = kMmaWarp + 1;              // 13: PV issuer
+constexpr int kThreads = 32 * (kPvWarp + 1);       // 448
+constexpr int kMathBar = 1;                        // named barrier of the 128 math threads
+constexpr int kEpiBar = 2;                         // of the epilogue (math and loader warps)
+constexpr int kEpiThreads = 32 * kMmaWarp;         // 384
+constexpr int kEpiGroups = kEpiThreads / 128;      // 3 groups of four warps (TMEM lane quarters)
+
+// Shared memory, offsets from a 1024-aligned base. The QK^T MMA reads 64 rows
+// past each Q atom (they only feed unused accumulator lanes); past the last
+// atom they land in the P buffers.
+constexpr int kAtomBytes = kRows * 128;            // 64 dims of a tile's rows
+constexpr int kSlotBytes = 8 * kAtomBytes;
+constexpr int kQ = 0;                              // 8 atoms x 64 heads x 128 B
+constexpr uint32_t kQBytes = kHeads * kLatent * 2;
+constexpr int kP = kQ + static_cast<int>(kQBytes); // 2 x (64 heads x 64 rows bf16)
+constexpr int kPBytes = kHeads * 128;
+constexpr int kKV = kP + 2 * kPBytes;              // the two slots
+constexpr int kKVBytes = kSlots * kSlotBytes;
+constexpr int kIds = kKV + kKVBytes;               // compacted latent rows
+constexpr int kMisc = kIds + kMaxKTokens * 4;
+constexpr int kMiscBytes = 1024;
+constexpr int kSmemBytes = kMisc + kMiscBytes + 1024;  // + alignment slack of the base
+constexpr int kTmemCols = 512;  // S[b]: cols [64 b, 64 b + 64); O^T slice m: [128 + 64 m, ...)
+
+// What a CTA sends to the one finishing dims [p D, p D + D), D = 512 / S: its
+// unnormalised O for those dims, per dim 64 heads x 2 bytes (the upper halves
+// of the fp32 values) and 64 heads x 1 byte (the next bits), then its (max,
+// sum) per head. 16-byte units are swizzled by the dim so that neighbouring
+// lanes touch different banks.
+__host__ __device__ constexpr int xchg_lo(int S) { return (kLatent / S) * 128; }
+__host__ __device__ constexpr int xchg_ml(int S) { return (kLatent / S) * 192; }
+__host__ __device__ constexpr int xchg_bytes(int S) { return xchg_ml(S) + kHeads * 8; }
+static_assert(2 * xchg_bytes(2) <= kKVBytes && 4 * xchg_bytes(4) <= kKVBytes &&
+                  kMaxAttnSplits * xchg_bytes(kMaxAttnSplits) <= kKVBytes,
+              "receive areas fit the slots");
+constexpr int kWgt = kP;  // [S][64] merge weights, in the P buffers
+static_assert(kMaxAttnSplits * kHeads * 4 <= 2 * kPBytes, "merge weights fit the P buffers");
+
+struct Misc {
+  uint64_t kv_full[kSlots], kv_empty[kSlots], s_full[2], s_free[2], p_full[2], p_empty[2];
+  uint64_t q_done, ids_ready;
+  uint64_t o_done;  // every MMA of the CTA has completed
+  uint32_t tmem_base;
+  int abort;
+  int n_sel;
+  int warp_cnt[4];
+  alignas(16) float alpha[kHeads];
+  alignas(16) float inv_l[kHeads];
+};
+static_assert(sizeof(Misc) <= kMiscBytes, "misc block");
+
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Misc* m,
+                                         DeviceStatus* st) {
+  return mbar_wait_abortable(bar, parity, &m->abort, st, SITE_ATTN);
+}
+
+// A loader lane's part of a tile: 16 bytes of codes and their scale byte of
+// four rows.
+struct Codes {
+  uint4 c[kWarpRows / 2];
+  uint32_t s[kWarpRows / 2];
+};
+
+// out[h0 + i][d] = v[i] for 16 heads, lane l holding dim d = d32 + l of a
+// 32-aligned range: three exchanges with lanes 1, 2 and 4 away leave each lane
+// 8 consecutive dims of two heads, so a warp writes 64 contiguous bytes of each of
+// eight heads by one 16-byte store a lane (2-byte stores, one head at a time,
+// take eight times as many).
+__device__ __forceinline__ void store_heads16(uint16_t* out, int h0, int d32, int lane,
+                                              const float (&v)[16]) {
+  const bool b0 = lane & 1, b1 = lane & 2, b2 = lane & 4;
+  uint32_t r[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {  // r[j]: head 2 j + b0, two dims
+    const __nv_bfloat162 x = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+    const uint32_t own = *reinterpret_cast<const uint32_t*>(&x);
+    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
+    r[j] = b0 ? prmt(got, own, 0x7632u) : prmt(own, got, 0x5410u);
+  }
+  uint2 u[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {  // u[j]: head 4 j + 2 b1 + b0, four dims
+    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, b1 ? r[2 * j] : r[2 * j + 1], 2);
+    u[j] = b1 ? make_uint2(got, r[2 * j + 1]) : make_uint2(r[2 * j], got);
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {  // head 8 j + 4 b2 + 2 b1 + b0, eight dims
+    const uint2 send = b2 ? u[2 * j] : u[2 * j + 1];
+    const uint2 got = make_uint2(__shfl_xor_sync(0xFFFFFFFFu, send.x, 4),
+                                 __shfl_xor_sync(0xFFFFFFFFu, send.y, 4));
+    const uint4 w = b2 ? make_uint4(got.x, got.y, u[2 * j + 1].x, u[2 * j + 1].y)
+                       : make_uint4(u[2 * j].x, u[2 * j].y, got.x, got.y);
+    *reinterpret_cast<uint4*>(out + static_cast<int64_t>(h0 + 8 * j + (lane & 7)) * kLatent + d32 +
+                              (lane & 24)) = w;
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    attn4_kernel(AttnArgs a, const __grid_constant__ CUtensorMap qmap) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (sbase - raw);
+  Misc* misc = reinterpret_cast<Misc*>(gbase + kMisc);
+  int32_t* ids = reinterpret_cast<int32_t*>(gbase + kIds);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int b = blockIdx.x;
+  const int split = blockIdx.y;  // rank in the cluster
+  const int S = a.splits;
+  const bool paired = S > 1;
+
+  if (tid == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&misc->kv_full[i], kLoadWarps);
+      mbar_init(&misc->kv_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&misc->s_full[i], 1);
+      mbar_init(&misc->s_free[i], 2);
+      mbar_init(&misc->p_full[i], 2);
+      mbar_init(&misc->p_empty[i], 1);
+    }
+    mbar_init(&misc->q_done, 1);     // the TMA loads of Q (expect-tx arrival + 64 KB)
+    mbar_init(&misc->ids_ready, 1);  // the math warps compacted the token ids
+    mbar_init(&misc->o_done, 1);     // the PV issuer's last commit
+    misc->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) tmem_alloc(&misc->tmem_base, kTmemCols);
+  griddep_launch_dependents();
+  tc_fence_before();
+  __syncthreads();  // barriers initialised, tensor memory allocated
+  tc_fence_after();
+  // The peers' barriers are initialised before any remote access: every
+  // thread arrives here and waits before its first cluster access.
+  if (paired) cluster_arrive_relaxed();
+
+  int n_vis = a.n_latents[b];
+  int n_sw = a.swa_len[b];
+  if (n_sw < 0 || n_sw > a.window) {
+    if (tid == 0 && split == 0) record_status(a.status, DSA_ERR_DEVICE_CHECK, SITE_ATTN, b);
+    n_sw = n_sw < 0 ? 0 : a.window;
+  }
+  if (n_vis > a.lat_stride) n_vis = static_cast<int>(a.lat_stride);
+  const bool paged = a.pages.table != nullptr;
+  const int64_t lat_row0 = paged ? 0 : static_cast<int64_t>(b) * a.lat_stride;
+  // This CTA's rows: its part of the window rows first (inputs of the step,
+  // read while the previous kernel still selects the tokens), then its part of
+  // the selected latents.
+  const int64_t wrow0 = static_cast<int64_t>(b) * a.window;
+  const int w_part = (n_sw + S - 1) / S;
+  const int w_begin = min(n_sw, split * w_part);
+  const int w_cnt = min(n_sw, w_begin + w_part) - w_begin;
+  auto sel_range = [&](int n_sel, int& s_begin, int& s_cnt) {
+    const int h = (n_sel + S - 1) / S;
+    s_begin = min(n_sel, split * h);
+    s_cnt = min(n_sel, s_begin + h) - s_begin;
+  };
+  const uint32_t tmem = misc->tmem_base;
+
+  if (warp == kLoadWarp0 && lane == 0) {
+    // Q does not depend on the ids: eight boxes of 64 heads x 64 dims, each
+    // landing as one 128-byte-swizzled atom of the QK^T A operand.
+    tma_prefetch_map(&qmap);
+    mbar_arrive_expect_tx(&misc->q_done, kQBytes);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      tma_load_2d(sbase + kQ + c * (kHeads * 128), &qmap, 64 * c, b * kHeads, &misc->q_done);
+    }
+  }
+
+  // Compact the valid token ids (>= 0 and < n_vis) in order (math threads,
+  // once the previous kernel's ids are final).
+  if (tid < 128) {
+    griddep_wait();
+    const int32_t* tk = a.token_ids + static_cast<int64_t>(b) * a.k_tokens;
+    constexpr int kPer = kMaxKTokens / 128;  // 4
+    int my[kPer];
+    int cnt = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = tid * kPer + j;
+      int id = -1;
+      if (i < a.k_tokens) {
+        id = tk[i];
+        if (id >= n_vis) {
+          if (split == 0) {
+            record_status(a.status, DSA_ERR_DEVICE_CHECK, SITE_ATTN, static_cast<uint32_t>(id));
+          }
+          id = -1;
+        }
+        if (paged && id >= 0) {
+          const int64_t row = paged_row(a.pages, b, id);
+          if (row < 0 && split == 0) {
+            record_status(a.status, DSA_ERR_DEVICE_CHECK, SITE_ATTN, static_cast<uint32_t>(id));
+          }
+          id = static_cast<int>(row);
+        }
+      }
+      my[j] = id;
+      cnt += id >= 0 ? 1 : 0;
+    }
+    int incl = cnt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    if (lane == 31) misc->warp_cnt[warp] = incl;
+    named_sync(kMathBar, 128);
+    int before = incl - cnt;
+    for (int w = 0; w < warp; ++w) before += misc->warp_cnt[w];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      if (my[j] >= 0) ids[before++] = my[j];
+    }
+    if (tid == 127) misc->n_sel = before;
+    named_sync(kMathBar, 128);
+    if (tid == 0) mbar_arrive(&misc->ids_ready);
+  }
+
+  // State the epilogue warps (math and loaders) share: the softmax statistics
+  // of head tid (threads 0..63), whether every wait succeeded, the tile count.
+  float m_run = -INFINITY, l_run = 0.f;
+  bool ok = true;
+  int n_tiles_e = 0;
+
+  if (warp >= kLoadWarp0 && warp < kMmaWarp) {
+    // ---------------- loaders ----------------
+    // Loader warp w fills rows [8 w, 8 w + 8) of every tile, two rows at a
+    // time: lane l reads bytes [16 j, 16 j + 16) of row 8 w + 2 i + l / 16,
+    // j = l % 16, which are its elements [32 j, 32 j + 32) under scale j. A
+    // tile's codes wait in registers (two sets) while the tile before is
+    // converted; rows without a source are zeros.
+    const int w = warp - kLoadWarp0;
+    const int j = lane & 15, half = lane >> 4;
+    const uint8_t* lat = reinterpret_cast<const uint8_t*>(a.latents);
+    const uint8_t* swa = reinterpret_cast<const uint8_t*>(a.swa);
+    bool have_ids = false;
+    int s_begin = 0, n_rows_cta = w_cnt, n_tiles = 0;
+    Codes even, odd;
+    auto load = [&](int t, Codes& k) {
+      // Lane r < 8 finds the source of row 8 w + r of the tile: its byte
+      // offset, or -1; bit 62 marks the window.
+      int64_t src_l = -1;
+      const int g = t * kRows + kWarpRows * w + lane;
+      if (lane < kWarpRows && g < n_rows_cta) {
+        if (g < w_cnt) {
+          const int64_t row = wrow0 + w_begin + g;
+          if (DSA_DCHECK(row >= 0 && row < a.swa_rows, a.status, SITE_ATTN, row)) {
+            src_l = row * kRow4Bytes | (int64_t{1} << 62);
+          }
+        } else {
+          const int64_t row = lat_row0 + ids[s_begin + g - w_cnt];
+          if (DSA_DCHECK(row >= 0 && row < a.lat_rows, a.status, SITE_ATTN, row)) {
+            src_l = row * kRow4Bytes;
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kWarpRows / 2; ++i) {
+        const int64_t src = __shfl_sync(0xFFFFFFFFu, src_l, 2 * i + half);
+        k.c[i] = make_uint4(0u, 0u, 0u, 0u);
+        k.s[i] = 0u;
+        if (src >= 0) {
+          const uint8_t* p = (src >> 62 ? swa : lat) + (src & ~(int64_t{1} << 62));
+          k.c[i] = __ldg(reinterpret_cast<const uint4*>(p) + j);
+          k.s[i] = __ldg(p + kRow4Codes + j);
+        }
+      }
+    };
+    auto store = [&](int t, const Codes& k) -> bool {
+      const int sl = t % kSlots;
+      if (t >= kSlots && !wait_bar(&misc->kv_empty[sl],
+                                   static_cast<uint32_t>(((t / kSlots) - 1) & 1), misc, a.status)) {
+        return false;
+      }
+      // Word i of the 16 bytes is 16-byte chunk 4 (j & 1) + i of the row in
+      // atom j / 2. The order is rotated by atom so that eight lanes (four
+      // atoms, both halves) write eight different 16-byte bank groups.
+      const int rot = (j >> 1) & 3;
+      const uint32_t base = sbase + kKV + sl * kSlotBytes +
+                            static_cast<uint32_t>(j >> 1) * kAtomBytes;
+#pragma unroll
+      for (int i = 0; i < kWarpRows / 2; ++i) {
+        uint4 c = k.c[i];
+        if (rot & 1) c = make_uint4(c.y, c.z, c.w, c.x);
+        if (rot & 2) c = make_uint4(c.z, c.w, c.x, c.y);
+        const uint32_t f = mx4_scale_bf16x2(k.s[i]);
+        const uint32_t row = static_cast<uint32_t>(kWarpRows * w + 2 * i + half);
+        const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const uint32_t chunk = 4u * (j & 1) + ((n + rot) & 3);
+          st_shared_v4(base + sw128_off(row, chunk), mx4_decode8(cw[n], f));
+        }
+      }
+      fence_proxy_async_smem();  // the MMAs read the tile through the async proxy
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&misc->kv_full[sl]);
+      return true;
+    };
+    // store tile t from the set its parity names
+    auto store_of = [&](int t) -> bool { return t & 1 ? store(t, odd) : store(t, even); };
+    int pending = -1;  // a tile read but not yet converted
+    for (int t = 0; ok; ++t) {
+      if (!have_ids && (t + 1) * kRows > w_cnt) {
+        // the window rows read so far need not wait for the ids
+        if (pending >= 0 && !store_of(pending)) ok = false;
+        pending = -1;
+        if (!ok || !wait_bar(&misc->ids_ready, 0u, misc, a.status)) {
+          ok = false;
+          break;
+        }
+        int s_cnt;
+        sel_range(misc->n_sel, s_begin, s_cnt);
+        n_rows_cta = w_cnt + s_cnt;
+        n_tiles = (n_rows_cta + kRows - 1) / kRows;
+        have_ids = true;
+      }
+      if (have_ids && t >= n_tiles) break;
+      if (t & 1) {
+        load(t, odd);
+      } else {
+        load(t, even);
+      }
+      if (pending >= 0 && !store_of(pending)) ok = false;
+      pending = t;
+    }
+    if (ok && pending >= 0 && !store_of(pending)) ok = false;
+    n_tiles_e = have_ids ? n_tiles : 0;
+  } else if (warp == kMmaWarp || warp == kPvWarp) {
+    // ---------------- MMA issuers ----------------
+    int n_tiles = 0;
+    if (lane == 0 && wait_bar(&misc->ids_ready, 0u, misc, a.status)) {
+      int s_begin, s_cnt;
+      sel_range(misc->n_sel, s_begin, s_cnt);
+      n_tiles = (w_cnt + s_cnt + kRows - 1) / kRows;
+    }
+    // PV(t) is issued only after the softmax of tile t, hence after QK^T(t)
+    // completed: its commit alone frees the tile's slot, and the PV issuer's
+    // last commit means every MMA of the CTA has completed.
+    if (lane == 0 && warp == kPvWarp) {
+      constexpr uint32_t idesc_o = mma_idesc(128, kHeads, true, true, false);
+      for (int t = 0; t < n_tiles; ++t) {
+        const int sb = t & 1, sl = t % kSlots;
+        if (!wait_bar(&misc->p_full[sb], static_cast<uint32_t>((t >> 1) & 1), misc, a.status)) {
+          break;
+        }
+        tc_fence_after();
+        fence_proxy_async_smem();
+        // Descriptors are built once and stepped by their start-address field
+        // (16-byte units; every operand lies below 256 KB, so no carry).
+        const uint64_t ad0 = sw128_desc(sbase + kKV + sl * kSlotBytes, kAtomBytes, 1024);
+        const uint64_t bd0 = sw128_desc(sbase + kP + sb * kPBytes, 16, 1024);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+#pragma unroll
+          for (int ks = 0; ks < kRows / 16; ++ks) {
+            const uint64_t ad = ad0 + ((m * 2 * kAtomBytes + ks * 16 * 128) >> 4);
+            const uint64_t bd = bd0 + ((ks * 32) >> 4);
+            mma_f16(tmem + 128 + 64 * m, ad, bd, idesc_o, (t > 0 || ks > 0) ? 1u : 0u);
+          }
+        }
+        mma_commit(&misc->kv_empty[sl]);
+        mma_commit(&misc->p_empty[sb]);
+      }
+      if (n_tiles > 0) mma_commit(&misc->o_done);  // arrives once every MMA has completed
+    }
+    if (lane == 0 && warp == kMmaWarp) {
+      constexpr uint32_t idesc_s = mma_idesc(128, kRows, true, false, false);
+      bool qk_ok = n_tiles == 0 || wait_bar(&misc->q_done, 0u, misc, a.status);
+      for (int t = 0; t < n_tiles && qk_ok; ++t) {
+        const int sl = t % kSlots, sb = t & 1;
+        if (!wait_bar(&misc->kv_full[sl], static_cast<uint32_t>((t / kSlots) & 1), misc,
+                      a.status) ||
+            (t >= 2 && !wait_bar(&misc->s_free[sb], static_cast<uint32_t>(((t >> 1) - 1) & 1),
+                                 misc, a.status))) {
+          qk_ok = false;
+          break;
+        }
+        tc_fence_after();
+        fence_proxy_async_smem();
+        const uint64_t ad0 = sw128_desc(sbase + kQ, 16, 1024);
+        const uint64_t bd0 = sw128_desc(sbase + kKV + sl * kSlotBytes, 16, 1024);
+#pragma unroll
+        for (int ks = 0; ks < kLatent / 16; ++ks) {
+          const uint64_t ad = ad0 + (((ks >> 2) * (kHeads * 128) + (ks & 3) * 32) >> 4);
+          const uint64_t bd = bd0 + (((ks >> 2) * kAtomBytes + (ks & 3) * 32) >> 4);
+          mma_f16(tmem + 64 * sb, ad, bd, idesc_s, ks > 0 ? 1u : 0u);
+        }
+        mma_commit(&misc->s_full[sb]);
+      }
+    }
+    __syncwarp();
+    if (paired) {
+      // the phases of the exchange below, which these warps only pass through
+      cluster_wait();
+      cluster_arrive();
+      cluster_wait();
+      cluster_arrive();
+    }
+  } else {
+    // ---------------- math: softmax, rescale ----------------
+    int s_begin, s_cnt;
+    sel_range(misc->n_sel, s_begin, s_cnt);
+    const int n_rows_cta = w_cnt + s_cnt;
+    const int n_tiles = (n_rows_cta + kRows - 1) / kRows;
+    // A failed (timed-out) wait makes `ok` false for good; the thread then
+    // skips the work but still reaches every named barrier.
+    n_tiles_e = n_tiles;
+    const uint32_t la = tmem_addr(tmem, static_cast<uint32_t>(32 * warp), 0);
+    const float sl = a.scale_log2;
+    // PV(j) is known complete through p_empty[j & 1], whose phases a thread
+    // consumes in order (at most one phase ahead of its last wait).
+    auto wait_pv = [&](int t) {
+      if (ok) {
+        ok = wait_bar(&misc->p_empty[t & 1], static_cast<uint32_t>((t >> 1) & 1), misc, a.status);
+      }
+    };
+    for (int t = 0; t < n_tiles; ++t) {
+      const int sb = t & 1;
+      const int valid = min(kRows, n_rows_cta - t * kRows);
+      float z[kRows];
+      float alpha = 1.f;
+      bool resc = false;
+      if (warp < 2) {
+        if (ok) {
+          ok = wait_bar(&misc->s_full[sb], static_cast<uint32_t>((t >> 1) & 1), misc, a.status);
+        }
+        tc_fence_after();
+        if (ok) {
+          load_scores<kRows>(la + 64 * sb, valid, z);
+          const float mt = max_scores<kRows>(z, sl);
+          if (t == 0) {
+            m_run = mt;
+          } else if (mt > m_run + 8.f) {
+            alpha = exp2f(m_run - mt);
+            m_run = mt;
+            resc = true;
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&misc->s_free[sb]);
+        misc->alpha[tid] = alpha;
+      }
+      // O^T holds PV(0..t-1); if any head's maximum moved, scale every head's
+      // column by its alpha (1 for heads whose maximum stayed).
+      const bool any_resc = named_sync_or(kMathBar, 128, resc);
+      if (any_resc) {
+        if (t > 0) wait_pv(t - 1);
+        tc_fence_after();
+        if (ok && t > 0) {
+#pragma unroll 1
+          for (int m = 0; m < 4; ++m) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              float v[16];
+              const uint32_t addr = la + 128 + 64 * m + 16 * c;
+              tmem_ld16(addr, v);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] *= misc->alpha[16 * c + i];
+              tmem_st16(addr, v);
+            }
+          }
+        }
+        tc_fence_before();
+        named_sync(kMathBar, 128);  // alpha is read by all before the next tile rewrites it
+      }
+      if (warp < 2) {
+        if (t >= 2) wait_pv(t - 2);  // P[sb] was last read by PV(t - 2)
+        if (ok) {
+          uint32_t pk[kRows / 2];
+          // the denominator sums the fp32 probabilities; the MMA takes them in
+          // bf16, the type of its other operand
+          l_run = l_run * alpha + exp_pack<kRows>(z, sl, m_run, pk);
+          const uint32_t pb = sbase + kP + sb * kPBytes;
+#pragma unroll
+          for (int c = 0; c < kRows / 8; ++c) {
+            st_shared_v4(pb + sw128_off(tid, c),
+                         make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]));
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&misc->p_full[sb]);
+      }
+    }
+  }
+
+  if (warp < kMmaWarp) {
+    // ---------------- epilogue (math and loader warps) ----------------
+    // Warp w reads TMEM lanes 32 (w % 4) .. + 31 (dims 128 m + 32 (w % 4) + lane of O^T
+    // slice m); the (slice, 16-head chunk) pairs are dealt to the three warps of a lane
+    // quarter in turn. The loops are rolled: the code runs once per CTA and is fetched
+    // cold.
+    const int grp = warp >> 2;
+    const int et0 = 32 * (warp & 3);  // first dim within a slice = TMEM lane
+    const uint32_t lq = tmem_addr(tmem, static_cast<uint32_t>(et0), 0);
+    const int n_tiles = n_tiles_e;
+    if (n_tiles > 0) {
+      if (ok) ok = wait_bar(&misc->o_done, 0u, misc, a.status);
+    } else if (ok) {
+      // no tiles: nothing else ordered the Q copies before the CTA's end
+      ok = wait_bar(&misc->q_done, 0u, misc, a.status);
+    }
+    tc_fence_after();
+    const bool have_o = ok && n_tiles > 0;
+    uint16_t* out = a.out + static_cast<int64_t>(b) * kHeads * kLatent;
+    auto load16 = [&](int m, int hc, float (&v)[16]) {
+      if (have_o) {
+        tmem_ld16(lq + 128 + 64 * m + 16 * hc, v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = 0.f;
+      }
+    };
+    auto scale16 = [&](float (&v)[16], uint32_t f, int hc) {
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const float4 w4 = ld_shared_f4(f + (16 * hc + i) * 4);
+        v[i] *= w4.x;
+        v[i + 1] *= w4.y;
+        v[i + 2] *= w4.z;
+        v[i + 3] *= w4.w;
+      }
+    };
+    if (!paired) {
+      if (warp < 2) {
+        misc->inv_l[tid] = l_run > 0.f ? 1.f / l_run : 0.f;
+        if (a.lse) {
+          a.lse[static_cast<int64_t>(b) * kHeads + tid] =
+              l_run > 0.f ? (m_run + log2f(l_run)) * 0.69314718055994531f : -INFINITY;
+        }
+      }
+      named_sync(kEpiBar, kEpiThreads);
+      const uint32_t inv_l_s = smem_u32(misc->inv_l);
+#pragma unroll 1
+      for (int i = grp; i < 16; i += kEpiGroups) {
+        float v[16];
+        load16(i >> 2, i & 3, v);
+        scale16(v, inv_l_s, i & 3);
+        store_heads16(out, 16 * (i & 3), 128 * (i >> 2) + et0, lane, v);
+      }
+    } else {
+      // CTA `split` finishes dims [split D, split D + D). A warp's 32 dims always
+      // go to one CTA. Each CTA writes its part for each peer straight into the
+      // peer's receive area (its slots, free once the peer's MMAs are done), and
+      // its own (max, sum) into its own, so the merge reads all alike.
+      const int D = kLatent / S;
+      const uint32_t pay = static_cast<uint32_t>(xchg_bytes(S));
+      const uint32_t off_lo = static_cast<uint32_t>(xchg_lo(S));
+      const uint32_t off_ml = static_cast<uint32_t>(xchg_ml(S));
+      const float m_own = have_o ? m_run : -INFINITY, l_own = have_o ? l_run : 0.f;
+      auto recv_slot = [&](int q) -> uint32_t {  // what CTA q sent, in this CTA
+        return sbase + kKV + static_cast<uint32_t>(q) * pay;
+      };
+      cluster_wait();  // phase 0: every CTA's barriers are initialised
+      if (warp < 2) {
+        float* t = reinterpret_cast<float*>(gbase + (recv_slot(split) - sbase) + off_ml);
+        t[2 * tid] = m_own;
+        t[2 * tid + 1] = l_own;
+      }
+      cluster_arrive();  // phase 1: every CTA's MMAs are done, so its slots may be written
+      cluster_wait();
+#pragma unroll 1
+      for (int i = grp; i < 16; i += kEpiGroups) {
+        const int m = i >> 2, hc = i & 3;
+        const int d = 128 * m + et0 + lane;
+        const int p = d / D;
+        if (p == split) continue;
+        const uint32_t dd = static_cast<uint32_t>(d - p * D);
+        const uint32_t area = mapa_shared(recv_slot(split), static_cast<uint32_t>(p));
+        float v[16];
+        load16(m, hc, v);
+        uint32_t hi[8], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          // the upper 24 bits, rounded half up (a carry into the exponent is right
+          // too; a NaN's bits take no carry)
+          uint32_t x[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float f = v[4 * e + k];
+            x[k] = f == f ? __float_as_uint(f) + 0x80u : 0x7FC00000u;
+          }
+          hi[2 * e] = prmt(x[0], x[1], 0x7632u);
+          hi[2 * e + 1] = prmt(x[2], x[3], 0x7632u);
+          lo[e] = prmt(prmt(x[0], x[1], 0x0051u), prmt(x[2], x[3], 0x0051u), 0x5410u);
+        }
+        const uint32_t row = area + dd * 128u;
+        st_cluster_u4(row + ((2u * hc) ^ (dd & 7u)) * 16u, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+        st_cluster_u4(row + ((2u * hc + 1u) ^ (dd & 7u)) * 16u,
+                      make_uint4(hi[4], hi[5], hi[6], hi[7]));
+        st_cluster_u4(area + off_lo + dd * 64u + (static_cast<uint32_t>(hc) ^ ((dd >> 1) & 3u)) * 16u,
+                      make_uint4(lo[0], lo[1], lo[2], lo[3]));
+      }
+      if (warp < 2) {
+        for (int p = 0; p < S; ++p) {
+          if (p == split) continue;
+          st_cluster_f32x2(mapa_shared(recv_slot(split) + off_ml + 8 * tid, static_cast<uint32_t>(p)),
+                           m_own, l_own);
+        }
+      }
+      cluster_arrive();  // phase 2: everything is written (release) ...
+      cluster_wait();    // ... and visible here (acquire)
+      // out = sum_q w_q O_q with w_q = 2^(m_q - M) / L, M = max_q m_q,
+      // L = sum_q 2^(m_q - M) l_q (a range without rows has l_q = 0).
+      float* wgt = reinterpret_cast<float*>(gbase + kWgt);  // [S][64]
+      if (warp < 2) {
+        auto ml = [&](int q) {  // sender q's (max, sum) of head tid
+          return reinterpret_cast<const float2*>(gbase + (recv_slot(q) - sbase) + off_ml)[tid];
+        };
+        float M = -INFINITY;
+#pragma unroll 1
+        for (int q = 0; q < S; ++q) {
+          const float2 x = ml(q);
+          if (x.y > 0.f) M = fmaxf(M, x.x);
+        }
+        float L = 0.f;
+#pragma unroll 1
+        for (int q = 0; q < S; ++q) {
+          const float2 x = ml(q);
+          const float e = x.y > 0.f ? exp2f(x.x - M) : 0.f;
+          wgt[q * kHeads + tid] = e;
+          L = fmaf(e, x.y, L);
+        }
+        const float inv_L = L > 0.f ? 1.f / L : 0.f;
+#pragma unroll 1
+        for (int q = 0; q < S; ++q) wgt[q * kHeads + tid] *= inv_L;
+        if (a.lse && split == 0) {
+          a.lse[static_cast<int64_t>(b) * kHeads + tid] =
+              L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+        }
+      }
+      named_sync(kEpiBar, kEpiThreads);
+      const uint32_t wgt_s = sbase + kWgt;
+#pragma unroll 1
+      for (int i = grp; i < 16; i += kEpiGroups) {
+        const int m = i >> 2, hc = i & 3;
+        const int d = 128 * m + et0 + lane;
+        if (d / D != split) continue;
+        const uint32_t dd = static_cast<uint32_t>(d - split * D);
+        float v[16];
+        load16(m, hc, v);
+        scale16(v, wgt_s + static_cast<uint32_t>(split * kHeads * 4), hc);
+#pragma unroll 1
+        for (int q = 0; q < S; ++q) {
+          if (q == split) continue;
+          const uint32_t area = recv_slot(q);
+          const uint32_t row = area + dd * 128u;
+          const uint4 x0 = ld_shared_v4(row + ((2u * hc) ^ (dd & 7u)) * 16u);
+          const uint4 x1 = ld_shared_v4(row + ((2u * hc + 1u) ^ (dd & 7u)) * 16u);
+          const uint4 y = ld_shared_v4(area + off_lo + dd * 64u +
+                                       (static_cast<uint32_t>(hc) ^ ((dd >> 1) & 3u)) * 16u);
+          const uint32_t hi[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+          const uint32_t lo[4] = {y.x, y.y, y.z, y.w};
+          const uint32_t wq = wgt_s + static_cast<uint32_t>(q * kHeads * 4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float4 w4 = ld_shared_f4(wq + (16 * hc + 4 * e) * 4);
+            // bytes: 0, the 8-bit part, the 16-bit part
+            const uint32_t b01 = hi[2 * e], b23 = hi[2 * e + 1], l4 = lo[e];
+            const float f0 = __uint_as_float(prmt(b01, l4, 0x1040u) & 0xFFFFFF00u);
+            const float f1 = __uint_as_float(prmt(b01, l4, 0x3250u) & 0xFFFFFF00u);
+            const float f2 = __uint_as_float(prmt(b23, l4, 0x1060u) & 0xFFFFFF00u);
+            const float f3 = __uint_as_float(prmt(b23, l4, 0x3270u) & 0xFFFFFF00u);
+            v[4 * e] = fmaf(w4.x, f0, v[4 * e]);
+            v[4 * e + 1] = fmaf(w4.y, f1, v[4 * e + 1]);
+            v[4 * e + 2] = fmaf(w4.z, f2, v[4 * e + 2]);
+            v[4 * e + 3] = fmaf(w4.w, f3, v[4 * e + 3]);
+          }
+        }
+        store_heads16(out, 16 * hc, 128 * m + et0, lane, v);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+  // The epilogue warps have waited for phase 2 (no peer writes this CTA any
+  // more); the MMA warps, which only arrived there, wait now.
+  if (paired && warp >= kMmaWarp) cluster_wait();
+}
+
+}  // namespace
+
+cudaError_t launch_attn4(const AttnArgs& a, cudaStream_t s) {
+  if (a.B == 0) return cudaSuccess;
+  if (a.prefill || (a.splits != 1 && a.splits != 2 && a.splits != 4 && a.splits != 8)) {
+    return cudaErrorInvalidValue;
+  }
+  CUtensorMap qmap;
+  memset(&qmap, 0, sizeof(qmap));
+  cudaError_t e = encode_tma_2d(&qmap, a.q, 2, kLatent, static_cast<uint64_t>(a.B) * kHeads,
+                                kLatent * 2, 64, kHeads);
+  if (e != cudaSuccess) return e;
+  AttnArgs args = a;
+  args.swa_rows = static_cast<int64_t>(a.B) * a.window;
+  static std::atomic<int> smem_set[64]{};
+  e = ensure_smem(reinterpret_cast<const void*>(attn4_kernel), kSmemBytes, smem_set);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attn4_kernel, dim3(a.B, a.splits), dim3(kThreads), kSmemBytes, s, a.splits,
+                    args, qmap);
+}
+
+}  // namespace dsa

@@ -21,7 +21,8 @@ namespace dsa {
 struct DeviceStatus {
   uint32_t code;  // 0 or the first dsa_status_t a kernel recorded
   uint32_t info;  // detail: (site << 24) | low bits of the offending value
-  uint32_t pad[2];
+  uint32_t ticket;  // CTAs of a step plan that have finished (zero between calls)
+  uint32_t pad;
 };
 
 // Sites recorded in DeviceStatus::info.
@@ -32,6 +33,8 @@ enum : uint32_t {
   SITE_ATTN = 4,
   SITE_PREFILL = 5,
   SITE_SELFTEST = 6,
+  SITE_PLAN = 7,
+  SITE_ROWS = 8,
 };
 
 __device__ __forceinline__ void record_status(DeviceStatus* st, uint32_t code, uint32_t site,

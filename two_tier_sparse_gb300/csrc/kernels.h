@@ -76,8 +76,8 @@ cudaError_t launch_pool(const PoolArgs& a, cudaStream_t s);
 
 // Cache append at the compression step: for each sequence whose token count
 // n completes a latent (n % ratio == 0), latent n / ratio - 1 becomes
-// RN_bf16(sum_i softmax(gate)_i kv_i) over its ratio positions, and its index
-// key row is copied in; n_lat_out[b] = n / ratio for the tail pooling after.
+// RN(sum_i softmax(gate)_i kv_i) over its ratio positions, rounded to the cache's
+// format, and its index key row is copied in; n_lat_out[b] = n / ratio for the tail pooling after.
 struct AppendArgs {
   int B;
   int ratio;                 // 1..32
@@ -87,7 +87,8 @@ struct AppendArgs {
   int fmt;
   const uint8_t* new_key;    // [B, row bytes] in the key format
   const uint8_t* new_scales; // [B, 4] (MX formats)
-  uint16_t* latents;
+  int kv_fmt;                // of the latents: bf16 or MXFP4
+  void* latents;
   int64_t lat_stride;
   uint8_t* key_data;
   uint8_t* key_scales;
@@ -274,6 +275,76 @@ cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s);
 // queries' clusters fit the device at once (attn_max_clusters).
 constexpr int kMaxAttnSplits = 8;
 int attn_max_clusters(int splits);
+// The same over a 4-bit cache (latents and swa are byte arrays of 272-byte
+// rows; decode only, any split).
+cudaError_t launch_attn4(const AttnArgs& a, cudaStream_t s);
+
+// KV rows written to / read from a cache of n_rows rows in format kv_fmt: row r
+// (of n, or of the first *n_valid) goes with cache row slots[r]; negative
+// slots are skipped.
+struct RowsArgs {
+  int n;
+  const int32_t* n_valid;  // device count of rows, or null
+  const void* rows;        // bf16, row r at r * row_stride elements (written by a read)
+  int64_t row_stride;
+  const int32_t* slots;
+  void* cache;
+  int64_t n_rows;
+  int kv_fmt;
+  float kv_scale;
+  DeviceStatus* status;
+};
+cudaError_t launch_kv_write(const RowsArgs& a, cudaStream_t s);
+cudaError_t launch_kv_read(const RowsArgs& a, cudaStream_t s);
+
+// One group of heads of a norm-and-rotate call (dsa_heads_t).
+struct NormRopeSeg {
+  const void* x;
+  void* out;
+  int64_t x_token_stride, x_head_stride, out_token_stride, out_head_stride;  // elements
+  const float* weight;  // [dim] or null
+  int heads, dim;
+  int lanes_log2;       // lanes of a warp that hold one head
+  int unit_end;         // units (warps' worth of heads) up to and with this group
+  int norm, rope, rope_start;
+  float eps, inv_dim;
+};
+struct NormRopeArgs {
+  int n;
+  const int32_t* n_valid;  // device count of tokens, or null
+  const int32_t* positions;
+  const double* inv_freq;  // [pairs]
+  int pairs, interleaved;
+  float rope_scale;
+  int units, units_per_cta;  // warps' worth of heads of a token, and of a CTA (set by the launch)
+  NormRopeSeg seg[DSA_MAX_HEAD_GROUPS];
+};
+cudaError_t launch_norm_rope(const NormRopeArgs& a, int dtype, int max_dim, cudaStream_t s);
+
+// The plan of a step (dsa_plan_step).
+struct PlanArgs {
+  int B, ratio, window;
+  const int32_t* n_tokens;
+  const int32_t* n_new;
+  int32_t* table;
+  int page_rows, pages_per_seq;
+  int64_t n_pages;
+  int32_t* ring;
+  const int64_t* ring_state;
+  int64_t* ring_state_out;
+  int32_t* n_tokens_out;
+  int32_t* n_latents;
+  int32_t* swa_len;
+  int32_t* cu_new;
+  int max_new;
+  int32_t* token_seq;
+  int32_t* positions;
+  int32_t* latent_slots;
+  int32_t* window_slots;
+  uint32_t* ticket;  // zero between calls
+  DeviceStatus* status;
+};
+cudaError_t launch_plan(const PlanArgs& a, cudaStream_t s);
 
 // block_ids[b] = 0, 1, ..., ceil(n_latents[b] / 8) - 1, then -1.
 cudaError_t launch_identity_blocks(const int32_t* n_latents, int B, int k_blocks,

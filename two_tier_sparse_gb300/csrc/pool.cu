@@ -4,7 +4,7 @@
 // is the block-key rule this library fixes), summed in fp32 in member order,
 // divided by the member count in fp32 and stored in the keys' own format:
 // bf16 round-to-nearest-even, or MXFP8 / MXFP4 by the OCP MX v1.0 conversion.
-#include "kernels.h"
+#include "kv_format.cuh"
 
 namespace dsa {
 
@@ -284,15 +284,31 @@ __global__ void __launch_bounds__(256) append_kernel(AppendArgs a) {
       acc[2 * k + 1] = fmaf(wi, bf16_bits_to_float(xs[k] >> 16), acc[2 * k + 1]);
     }
   }
-  uint32_t out[8];
+  if (a.kv_fmt == DSA_KV_MXFP4) {
+    // lanes 2 g and 2 g + 1 hold the 32 elements of scale g
+    uint32_t amax = 0;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(acc[2 * k], acc[2 * k + 1]);
-    out[k] = *reinterpret_cast<const uint32_t*>(&h);
+    for (int d = 0; d < 16; ++d) amax = max(amax, __float_as_uint(acc[d]) & 0x7FFFFFFFu);
+    amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+    const uint32_t scale = mx4_scale(amax);
+    const float lo[8] = {acc[0], acc[1], acc[2], acc[3], acc[4], acc[5], acc[6], acc[7]};
+    const float hi[8] = {acc[8], acc[9], acc[10], acc[11], acc[12], acc[13], acc[14], acc[15]};
+    uint8_t* row = static_cast<uint8_t*>(a.latents) + lrow * kRow4Bytes;
+    *reinterpret_cast<uint2*>(row + 8 * lane) =
+        make_uint2(mx4_encode8(lo, scale), mx4_encode8(hi, scale));
+    if ((lane & 1) == 0) row[kRow4Codes + (lane >> 1)] = static_cast<uint8_t>(scale);
+  } else {
+    uint32_t out[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(acc[2 * k], acc[2 * k + 1]);
+      out[k] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    uint4* dst =
+        reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.latents) + lrow * kLatent + 16 * lane);
+    dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
+    dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
   }
-  uint4* dst = reinterpret_cast<uint4*>(a.latents + lrow * kLatent + 16 * lane);
-  dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
-  dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
   // the index key row (and its scales)
   const int row_bytes = a.fmt == DSA_FMT_BF16 ? 256 : (a.fmt == DSA_FMT_MXFP8 ? 128 : 64);
   if (lane * 16 < row_bytes) {
