@@ -2,7 +2,8 @@
 // heads over the selected latents and the sliding window under one softmax,
 // the rows e2m1 codes with a power-of-two scale per 32 elements.
 //
-//   S   = Q . KV^T    (M = 128 with the 64 heads in lanes 0..63, N = 64 rows, K = 512)
+//   S   = Q . KV^T    (.ws, M = 64 heads, N = 64 rows, K = 512: rows 0..31 in lanes 0..63,
+//                      rows 32..63 in lanes 64..127, 32 columns)
 //   O^T += KV^T . P^T (four M = 128 slices of the 512 latent dims, N = 64 heads,
 //                      K = 64 rows; the KV tile is read as an MN-major operand)
 //
@@ -10,11 +11,16 @@
 // loader warps read a tile's codes (16 bytes a lane: 32 elements, one scale)
 // while they convert the tile before it to bf16 into a swizzled operand slot.
 // bf16 holds every code times every scale exactly, so Q stays as it is given
-// and the MMAs see the cache's own values. Tiles have 64 rows (two slots of
-// 64 KB): the MMAs here are bound by the operands they read from shared memory
-// (M x K + N x K elements at 128 bytes a clock), which makes a QK^T step over
-// 32 rows cost as much as one over 64; a row's bytes no longer set the pace,
-// so nothing is gained by smaller tiles.
+// and the MMAs see the cache's own values.
+//
+// The MMAs are bound by the operands they read from shared memory at 128 bytes
+// a clock (a step of K = 16 measured 31 clocks for M = 64, N = 64, 46 for
+// M = 128, N = 64, whose extra lanes would hold no heads), provided that a
+// converged warp issues them with one lane elected: from a lane that has
+// branched off, a step took 58, descriptors moving through vector registers.
+// 64 rows a tile use the Q operand twice as well as 32. The weight-stationary
+// form's layout gives every math thread 32 scores of one head, so four warps
+// share the softmax.
 //
 // The split over a cluster of S CTAs, the lazy softmax maximum and the roles
 // are those of the attention over bf16 rows. The partial outputs that the CTAs
@@ -44,9 +50,7 @@ constexpr int kEpiBar = 2;                         // of the epilogue (math and 
 constexpr int kEpiThreads = 32 * kMmaWarp;         // 384
 constexpr int kEpiGroups = kEpiThreads / 128;      // 3 groups of four warps (TMEM lane quarters)
 
-// Shared memory, offsets from a 1024-aligned base. The QK^T MMA reads 64 rows
-// past each Q atom (they only feed unused accumulator lanes); past the last
-// atom they land in the P buffers.
+// Shared memory, offsets from a 1024-aligned base.
 constexpr int kAtomBytes = kRows * 128;            // 64 dims of a tile's rows
 constexpr int kSlotBytes = 8 * kAtomBytes;
 constexpr int kQ = 0;                              // 8 atoms x 64 heads x 128 B
@@ -57,16 +61,16 @@ constexpr int kKV = kP + 2 * kPBytes;              // the two slots
 constexpr int kKVBytes = kSlots * kSlotBytes;
 constexpr int kIds = kKV + kKVBytes;               // compacted latent rows
 constexpr int kMisc = kIds + kMaxKTokens * 4;
-constexpr int kMiscBytes = 1024;
+constexpr int kMiscBytes = 2048;
 constexpr int kSmemBytes = kMisc + kMiscBytes + 1024;  // + alignment slack of the base
-constexpr int kTmemCols = 512;  // S[b]: cols [64 b, 64 b + 64); O^T slice m: [128 + 64 m, ...)
+constexpr int kTmemCols = 512;  // S[b]: cols [32 b, 32 b + 32); O^T slice m: [kTmemO + 64 m, ...)
+constexpr int kTmemO = 64;
 
-// What a CTA sends to the one finishing dims [p D, p D + D), D = 512 / S: its
-// unnormalised O for those dims, per dim 64 heads x 2 bytes (the upper halves
-// of the fp32 values) and 64 heads x 1 byte (the next bits), then its (max,
-// sum) per head. 16-byte units are swizzled by the dim so that neighbouring
-// lanes touch different banks.
-__host__ __device__ constexpr int xchg_lo(int S) { return (kLatent / S) * 128; }
+// What a CTA gives the one finishing dims [p D, p D + D), D = 512 / S (itself
+// included): its unnormalised O for those dims, then its (max, sum) per head.
+// O lies in planes of D x 16 bytes: plane u < 8 the upper 16 bits of heads
+// 8 u .. 8 u + 7 for each dim, plane 8 + u the next 8 bits of heads 16 u ..
+// 16 u + 15, so that a warp (32 dims) writes and reads 512 contiguous bytes.
 __host__ __device__ constexpr int xchg_ml(int S) { return (kLatent / S) * 192; }
 __host__ __device__ constexpr int xchg_bytes(int S) { return xchg_ml(S) + kHeads * 8; }
 static_assert(2 * xchg_bytes(2) <= kKVBytes && 4 * xchg_bytes(4) <= kKVBytes &&
@@ -83,14 +87,44 @@ struct Misc {
   int abort;
   int n_sel;
   int warp_cnt[4];
+  float mx[2][2][kHeads];  // a tile's largest score of each head in rows 0..31 and 32..63
   alignas(16) float alpha[kHeads];
   alignas(16) float inv_l[kHeads];
 };
 static_assert(sizeof(Misc) <= kMiscBytes, "misc block");
 
+// A converged warp's bounded wait; every lane gets the same answer (a lane whose
+// wait ran out takes the warp with it), so that warp-wide instructions after it
+// stay converged.
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Misc* m,
                                          DeviceStatus* st) {
-  return mbar_wait_abortable(bar, parity, &m->abort, st, SITE_ATTN);
+  return __all_sync(0xFFFFFFFFu, mbar_wait_abortable(bar, parity, &m->abort, st, SITE_ATTN));
+}
+
+// MMAs and commits of a converged warp, issued by one elected lane (the same
+// lane each time): the operands stay in uniform registers.
+__device__ __forceinline__ void mma_f16_warp(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                             uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ws_f16_warp(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                                uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.mma.ws.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit_warp(uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+          smem_u32(bar))
+      : "memory");
 }
 
 // A loader lane's part of a tile: 16 bytes of codes and their scale byte of
@@ -100,38 +134,36 @@ struct Codes {
   uint32_t s[kWarpRows / 2];
 };
 
-// out[h0 + i][d] = v[i] for 16 heads, lane l holding dim d = d32 + l of a
+// out[h0 + i][d] = v[i] for 8 heads, lane l holding dim d = d32 + l of a
 // 32-aligned range: three exchanges with lanes 1, 2 and 4 away leave each lane
-// 8 consecutive dims of two heads, so a warp writes 64 contiguous bytes of each of
+// 8 consecutive dims of one head, so a warp writes 64 contiguous bytes of each of
 // eight heads by one 16-byte store a lane (2-byte stores, one head at a time,
 // take eight times as many).
-__device__ __forceinline__ void store_heads16(uint16_t* out, int h0, int d32, int lane,
-                                              const float (&v)[16]) {
+__device__ __forceinline__ void store_heads8(uint16_t* out, int h0, int d32, int lane,
+                                             const float (&v)[8]) {
   const bool b0 = lane & 1, b1 = lane & 2, b2 = lane & 4;
-  uint32_t r[8];
+  uint32_t r[4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {  // r[j]: head 2 j + b0, two dims
+  for (int j = 0; j < 4; ++j) {  // r[j]: head 2 j + b0, two dims
     const __nv_bfloat162 x = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
     const uint32_t own = *reinterpret_cast<const uint32_t*>(&x);
     const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
     r[j] = b0 ? prmt(got, own, 0x7632u) : prmt(own, got, 0x5410u);
   }
-  uint2 u[4];
+  uint2 u[2];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {  // u[j]: head 4 j + 2 b1 + b0, four dims
+  for (int j = 0; j < 2; ++j) {  // u[j]: head 4 j + 2 b1 + b0, four dims
     const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, b1 ? r[2 * j] : r[2 * j + 1], 2);
     u[j] = b1 ? make_uint2(got, r[2 * j + 1]) : make_uint2(r[2 * j], got);
   }
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {  // head 8 j + 4 b2 + 2 b1 + b0, eight dims
-    const uint2 send = b2 ? u[2 * j] : u[2 * j + 1];
-    const uint2 got = make_uint2(__shfl_xor_sync(0xFFFFFFFFu, send.x, 4),
-                                 __shfl_xor_sync(0xFFFFFFFFu, send.y, 4));
-    const uint4 w = b2 ? make_uint4(got.x, got.y, u[2 * j + 1].x, u[2 * j + 1].y)
-                       : make_uint4(u[2 * j].x, u[2 * j].y, got.x, got.y);
-    *reinterpret_cast<uint4*>(out + static_cast<int64_t>(h0 + 8 * j + (lane & 7)) * kLatent + d32 +
-                              (lane & 24)) = w;
-  }
+  // head 4 b2 + 2 b1 + b0, eight dims
+  const uint2 send = b2 ? u[0] : u[1];
+  const uint2 got = make_uint2(__shfl_xor_sync(0xFFFFFFFFu, send.x, 4),
+                               __shfl_xor_sync(0xFFFFFFFFu, send.y, 4));
+  const uint4 w = b2 ? make_uint4(got.x, got.y, u[1].x, u[1].y)
+                     : make_uint4(u[0].x, u[0].y, got.x, got.y);
+  *reinterpret_cast<uint4*>(out + static_cast<int64_t>(h0 + (lane & 7)) * kLatent + d32 +
+                            (lane & 24)) = w;
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -155,8 +187,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&misc->s_full[i], 1);
-      mbar_init(&misc->s_free[i], 2);
-      mbar_init(&misc->p_full[i], 2);
+      mbar_init(&misc->s_free[i], 4);
+      mbar_init(&misc->p_full[i], 4);
       mbar_init(&misc->p_empty[i], 1);
     }
     mbar_init(&misc->q_done, 1);     // the TMA loads of Q (expect-tx arrival + 64 KB)
@@ -277,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint8_t* swa = reinterpret_cast<const uint8_t*>(a.swa);
     bool have_ids = false;
     int s_begin = 0, n_rows_cta = w_cnt, n_tiles = 0;
-    Codes even, odd;
+    Codes cur, nxt;
     auto load = [&](int t, Codes& k) {
       // Lane r < 8 finds the source of row 8 w + r of the tile: its byte
       // offset, or -1; bit 62 marks the window.
@@ -339,15 +371,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&misc->kv_full[sl]);
       return true;
     };
-    // store tile t from the set its parity names
-    auto store_of = [&](int t) -> bool { return t & 1 ? store(t, odd) : store(t, even); };
-    int pending = -1;  // a tile read but not yet converted
-    for (int t = 0; ok; ++t) {
-      if (!have_ids && (t + 1) * kRows > w_cnt) {
-        // the window rows read so far need not wait for the ids
-        if (pending >= 0 && !store_of(pending)) ok = false;
-        pending = -1;
-        if (!ok || !wait_bar(&misc->ids_ready, 0u, misc, a.status)) {
+    // Tile `stored` (in cur) is converted once tile `stored + 1` (in nxt) is on its way;
+    // when the next tile waits for the ids, the one at hand is converted first.
+    int loaded = 0, stored = 0;  // tiles read, tiles converted
+    while (ok) {
+      if (!have_ids && (loaded + 1) * kRows > w_cnt &&
+          (loaded == stored ||
+           __all_sync(0xFFFFFFFFu, mbar_try_wait(smem_u32(&misc->ids_ready), 0u)))) {
+        if (!wait_bar(&misc->ids_ready, 0u, misc, a.status)) {
           ok = false;
           break;
         }
@@ -357,21 +388,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         n_tiles = (n_rows_cta + kRows - 1) / kRows;
         have_ids = true;
       }
-      if (have_ids && t >= n_tiles) break;
-      if (t & 1) {
-        load(t, odd);
-      } else {
-        load(t, even);
+      const bool more = have_ids ? loaded < n_tiles : (loaded + 1) * kRows <= w_cnt;
+      if (loaded == stored) {
+        if (!more) break;
+        load(loaded++, cur);
+        continue;
       }
-      if (pending >= 0 && !store_of(pending)) ok = false;
-      pending = t;
+      const bool ahead = more && loaded == stored + 1;
+      if (ahead) load(loaded++, nxt);
+      if (!store(stored++, cur)) ok = false;
+      if (ahead) cur = nxt;
     }
-    if (ok && pending >= 0 && !store_of(pending)) ok = false;
     n_tiles_e = have_ids ? n_tiles : 0;
   } else if (warp == kMmaWarp || warp == kPvWarp) {
     // ---------------- MMA issuers ----------------
     int n_tiles = 0;
-    if (lane == 0 && wait_bar(&misc->ids_ready, 0u, misc, a.status)) {
+    if (wait_bar(&misc->ids_ready, 0u, misc, a.status)) {
       int s_begin, s_cnt;
       sel_range(misc->n_sel, s_begin, s_cnt);
       n_tiles = (w_cnt + s_cnt + kRows - 1) / kRows;
@@ -379,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // PV(t) is issued only after the softmax of tile t, hence after QK^T(t)
     // completed: its commit alone frees the tile's slot, and the PV issuer's
     // last commit means every MMA of the CTA has completed.
-    if (lane == 0 && warp == kPvWarp) {
+    if (warp == kPvWarp) {
       constexpr uint32_t idesc_o = mma_idesc(128, kHeads, true, true, false);
       for (int t = 0; t < n_tiles; ++t) {
         const int sb = t & 1, sl = t % kSlots;
@@ -398,16 +430,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int ks = 0; ks < kRows / 16; ++ks) {
             const uint64_t ad = ad0 + ((m * 2 * kAtomBytes + ks * 16 * 128) >> 4);
             const uint64_t bd = bd0 + ((ks * 32) >> 4);
-            mma_f16(tmem + 128 + 64 * m, ad, bd, idesc_o, (t > 0 || ks > 0) ? 1u : 0u);
+            mma_f16_warp(tmem + kTmemO + 64 * m, ad, bd, idesc_o, (t > 0 || ks > 0) ? 1u : 0u);
           }
         }
-        mma_commit(&misc->kv_empty[sl]);
-        mma_commit(&misc->p_empty[sb]);
+        mma_commit_warp(&misc->kv_empty[sl]);
+        mma_commit_warp(&misc->p_empty[sb]);
       }
-      if (n_tiles > 0) mma_commit(&misc->o_done);  // arrives once every MMA has completed
-    }
-    if (lane == 0 && warp == kMmaWarp) {
-      constexpr uint32_t idesc_s = mma_idesc(128, kRows, true, false, false);
+      if (n_tiles > 0) mma_commit_warp(&misc->o_done);  // arrives once every MMA has completed
+    } else {
+      constexpr uint32_t idesc_s = mma_idesc(kHeads, kRows, true, false, false);
       bool qk_ok = n_tiles == 0 || wait_bar(&misc->q_done, 0u, misc, a.status);
       for (int t = 0; t < n_tiles && qk_ok; ++t) {
         const int sl = t % kSlots, sb = t & 1;
@@ -426,9 +457,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int ks = 0; ks < kLatent / 16; ++ks) {
           const uint64_t ad = ad0 + (((ks >> 2) * (kHeads * 128) + (ks & 3) * 32) >> 4);
           const uint64_t bd = bd0 + (((ks >> 2) * kAtomBytes + (ks & 3) * 32) >> 4);
-          mma_f16(tmem + 64 * sb, ad, bd, idesc_s, ks > 0 ? 1u : 0u);
+          mma_ws_f16_warp(tmem + 32 * sb, ad, bd, idesc_s, ks > 0 ? 1u : 0u);
         }
-        mma_commit(&misc->s_full[sb]);
+        mma_commit_warp(&misc->s_full[sb]);
       }
     }
     __syncwarp();
@@ -448,7 +479,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // A failed (timed-out) wait makes `ok` false for good; the thread then
     // skips the work but still reaches every named barrier.
     n_tiles_e = n_tiles;
+    // Thread (half, h) has head h's scores of rows 32 half .. 32 half + 31 of each
+    // tile, and its share of the head's sum.
     const uint32_t la = tmem_addr(tmem, static_cast<uint32_t>(32 * warp), 0);
+    const int half = warp >> 1, h = tid & (kHeads - 1);
     const float sl = a.scale_log2;
     // PV(j) is known complete through p_empty[j & 1], whose phases a thread
     // consumes in order (at most one phase ahead of its last wait).
@@ -457,86 +491,90 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait_bar(&misc->p_empty[t & 1], static_cast<uint32_t>((t >> 1) & 1), misc, a.status);
       }
     };
+    constexpr int kHalf = kRows / 2;
     for (int t = 0; t < n_tiles; ++t) {
       const int sb = t & 1;
-      const int valid = min(kRows, n_rows_cta - t * kRows);
-      float z[kRows];
-      float alpha = 1.f;
-      bool resc = false;
-      if (warp < 2) {
-        if (ok) {
-          ok = wait_bar(&misc->s_full[sb], static_cast<uint32_t>((t >> 1) & 1), misc, a.status);
-        }
-        tc_fence_after();
-        if (ok) {
-          load_scores<kRows>(la + 64 * sb, valid, z);
-          const float mt = max_scores<kRows>(z, sl);
-          if (t == 0) {
-            m_run = mt;
-          } else if (mt > m_run + 8.f) {
+      const int valid = n_rows_cta - t * kRows - kHalf * half;
+      float z[kHalf];
+      float mt = -INFINITY, alpha = 1.f;
+      if (ok) ok = wait_bar(&misc->s_full[sb], static_cast<uint32_t>((t >> 1) & 1), misc, a.status);
+      tc_fence_after();
+      if (ok) {
+        load_scores<kHalf>(la + 32 * sb, valid, z);
+        mt = max_scores<kHalf>(z, sl);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&misc->s_free[sb]);
+      // The buffer of tile t - 2 is free: its readers have passed tile t - 1's barrier.
+      misc->mx[sb][half][h] = mt;
+      // If any head's maximum moved by more than 2^8 (or there is none yet), both halves
+      // take the larger one.
+      if (named_sync_or(kMathBar, 128, t == 0 || mt > m_run + 8.f)) {
+        mt = fmaxf(mt, misc->mx[sb][half ^ 1][h]);
+        if (t == 0) {
+          m_run = mt;
+        } else {
+          if (mt > m_run + 8.f) {
             alpha = exp2f(m_run - mt);
             m_run = mt;
-            resc = true;
           }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&misc->s_free[sb]);
-        misc->alpha[tid] = alpha;
-      }
-      // O^T holds PV(0..t-1); if any head's maximum moved, scale every head's
-      // column by its alpha (1 for heads whose maximum stayed).
-      const bool any_resc = named_sync_or(kMathBar, 128, resc);
-      if (any_resc) {
-        if (t > 0) wait_pv(t - 1);
-        tc_fence_after();
-        if (ok && t > 0) {
+          // O^T holds PV(0..t-1): scale every head's column by its alpha (1 for heads
+          // whose maximum stayed).
+          if (half == 0) misc->alpha[h] = alpha;
+          wait_pv(t - 1);
+          tc_fence_after();
+          named_sync(kMathBar, 128);
+          if (ok) {
 #pragma unroll 1
-          for (int m = 0; m < 4; ++m) {
+            for (int m = 0; m < 4; ++m) {
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                float v[16];
+                const uint32_t addr = la + kTmemO + 64 * m + 16 * c;
+                tmem_ld16(addr, v);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              float v[16];
-              const uint32_t addr = la + 128 + 64 * m + 16 * c;
-              tmem_ld16(addr, v);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] *= misc->alpha[16 * c + i];
-              tmem_st16(addr, v);
+                for (int i = 0; i < 16; ++i) v[i] *= misc->alpha[16 * c + i];
+                tmem_st16(addr, v);
+              }
             }
           }
+          tc_fence_before();
+          named_sync(kMathBar, 128);  // alpha is read by all before the next tile rewrites it
         }
-        tc_fence_before();
-        named_sync(kMathBar, 128);  // alpha is read by all before the next tile rewrites it
       }
-      if (warp < 2) {
-        if (t >= 2) wait_pv(t - 2);  // P[sb] was last read by PV(t - 2)
-        if (ok) {
-          uint32_t pk[kRows / 2];
-          // the denominator sums the fp32 probabilities; the MMA takes them in
-          // bf16, the type of its other operand
-          l_run = l_run * alpha + exp_pack<kRows>(z, sl, m_run, pk);
-          const uint32_t pb = sbase + kP + sb * kPBytes;
+      if (t >= 2) wait_pv(t - 2);  // P[sb] was last read by PV(t - 2)
+      if (ok) {
+        uint32_t pk[kHalf / 2];
+        // the denominator sums the fp32 probabilities; the MMA takes them in
+        // bf16, the type of its other operand
+        l_run = l_run * alpha + exp_pack<kHalf>(z, sl, m_run, pk);
+        const uint32_t pb = sbase + kP + sb * kPBytes;
 #pragma unroll
-          for (int c = 0; c < kRows / 8; ++c) {
-            st_shared_v4(pb + sw128_off(tid, c),
-                         make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]));
-          }
+        for (int c = 0; c < kHalf / 8; ++c) {
+          st_shared_v4(pb + sw128_off(h, 4 * half + c),
+                       make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]));
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&misc->p_full[sb]);
       }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&misc->p_full[sb]);
     }
+    // the two halves' sums (the order is fixed)
+    if (half == 1) misc->mx[0][0][h] = l_run;
+    named_sync(kMathBar, 128);
+    if (half == 0) l_run += misc->mx[0][0][h];
   }
 
   if (warp < kMmaWarp) {
     // ---------------- epilogue (math and loader warps) ----------------
     // Warp w reads TMEM lanes 32 (w % 4) .. + 31 (dims 128 m + 32 (w % 4) + lane of O^T
-    // slice m); the (slice, 16-head chunk) pairs are dealt to the three warps of a lane
+    // slice m); the (slice, 32 heads) pairs are dealt to the three warps of a lane
     // quarter in turn. The loops are rolled: the code runs once per CTA and is fetched
     // cold.
     const int grp = warp >> 2;
     const int et0 = 32 * (warp & 3);  // first dim within a slice = TMEM lane
-    const uint32_t lq = tmem_addr(tmem, static_cast<uint32_t>(et0), 0);
+    const uint32_t lq = tmem_addr(tmem, static_cast<uint32_t>(et0), kTmemO);
     const int n_tiles = n_tiles_e;
     if (n_tiles > 0) {
       if (ok) ok = wait_bar(&misc->o_done, 0u, misc, a.status);
@@ -547,22 +585,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const bool have_o = ok && n_tiles > 0;
     uint16_t* out = a.out + static_cast<int64_t>(b) * kHeads * kLatent;
-    auto load16 = [&](int m, int hc, float (&v)[16]) {
+    auto load32 = [&](int m, int hp, float (&v)[32]) {  // heads 32 hp .. + 31
       if (have_o) {
-        tmem_ld16(lq + 128 + 64 * m + 16 * hc, v);
+        tmem_ld32(lq + 64 * m + 32 * hp, v);
       } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = 0.f;
-      }
-    };
-    auto scale16 = [&](float (&v)[16], uint32_t f, int hc) {
-#pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        const float4 w4 = ld_shared_f4(f + (16 * hc + i) * 4);
-        v[i] *= w4.x;
-        v[i + 1] *= w4.y;
-        v[i + 2] *= w4.z;
-        v[i + 3] *= w4.w;
+        for (int i = 0; i < 32; ++i) v[i] = 0.f;
       }
     };
     if (!paired) {
@@ -576,68 +604,72 @@ __global__ void __launch_bounds__(kThreads, 1)
       named_sync(kEpiBar, kEpiThreads);
       const uint32_t inv_l_s = smem_u32(misc->inv_l);
 #pragma unroll 1
-      for (int i = grp; i < 16; i += kEpiGroups) {
-        float v[16];
-        load16(i >> 2, i & 3, v);
-        scale16(v, inv_l_s, i & 3);
-        store_heads16(out, 16 * (i & 3), 128 * (i >> 2) + et0, lane, v);
+      for (int i = grp; i < 8; i += kEpiGroups) {
+        float v[32];
+        load32(i >> 1, i & 1, v);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float o[8];
+#pragma unroll
+          for (int e = 0; e < 8; e += 4) {
+            const float4 f = ld_shared_f4(inv_l_s + (32 * (i & 1) + 8 * c + e) * 4);
+            o[e] = v[8 * c + e] * f.x;
+            o[e + 1] = v[8 * c + e + 1] * f.y;
+            o[e + 2] = v[8 * c + e + 2] * f.z;
+            o[e + 3] = v[8 * c + e + 3] * f.w;
+          }
+          store_heads8(out, 32 * (i & 1) + 8 * c, 128 * (i >> 1) + et0, lane, o);
+        }
       }
     } else {
-      // CTA `split` finishes dims [split D, split D + D). A warp's 32 dims always
-      // go to one CTA. Each CTA writes its part for each peer straight into the
-      // peer's receive area (its slots, free once the peer's MMAs are done), and
-      // its own (max, sum) into its own, so the merge reads all alike.
+      // CTA `split` finishes dims [split D, split D + D). Each CTA writes its part for
+      // each CTA straight into that one's receive area (its slots, free once its MMAs
+      // are done). A warp's 32 dims always go to one CTA.
       const int D = kLatent / S;
       const uint32_t pay = static_cast<uint32_t>(xchg_bytes(S));
-      const uint32_t off_lo = static_cast<uint32_t>(xchg_lo(S));
       const uint32_t off_ml = static_cast<uint32_t>(xchg_ml(S));
+      const uint32_t plane = static_cast<uint32_t>(D) * 16u;
       const float m_own = have_o ? m_run : -INFINITY, l_own = have_o ? l_run : 0.f;
       auto recv_slot = [&](int q) -> uint32_t {  // what CTA q sent, in this CTA
         return sbase + kKV + static_cast<uint32_t>(q) * pay;
       };
-      cluster_wait();  // phase 0: every CTA's barriers are initialised
-      if (warp < 2) {
-        float* t = reinterpret_cast<float*>(gbase + (recv_slot(split) - sbase) + off_ml);
-        t[2 * tid] = m_own;
-        t[2 * tid + 1] = l_own;
-      }
+      cluster_wait();    // phase 0: every CTA's barriers are initialised
       cluster_arrive();  // phase 1: every CTA's MMAs are done, so its slots may be written
       cluster_wait();
 #pragma unroll 1
-      for (int i = grp; i < 16; i += kEpiGroups) {
-        const int m = i >> 2, hc = i & 3;
+      for (int i = grp; i < 8; i += kEpiGroups) {
+        const int m = i >> 1, hp = i & 1;
         const int d = 128 * m + et0 + lane;
         const int p = d / D;
-        if (p == split) continue;
-        const uint32_t dd = static_cast<uint32_t>(d - p * D);
-        const uint32_t area = mapa_shared(recv_slot(split), static_cast<uint32_t>(p));
-        float v[16];
-        load16(m, hc, v);
-        uint32_t hi[8], lo[4];
+        const uint32_t area = mapa_shared(recv_slot(split), static_cast<uint32_t>(p)) +
+                              static_cast<uint32_t>(d - p * D) * 16u;
+        float v[32];
+        load32(m, hp, v);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          // the upper 24 bits, rounded half up (a carry into the exponent is right
-          // too; a NaN's bits take no carry)
-          uint32_t x[4];
+        for (int c = 0; c < 2; ++c) {  // 16 heads
+          uint32_t hi[8], lo[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float f = v[4 * e + k];
-            x[k] = f == f ? __float_as_uint(f) + 0x80u : 0x7FC00000u;
+          for (int e = 0; e < 4; ++e) {
+            // the upper 24 bits, rounded half up (a carry into the exponent is right
+            // too; a NaN's bits take no carry)
+            uint32_t x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float f = v[16 * c + 4 * e + k];
+              x[k] = f == f ? __float_as_uint(f) + 0x80u : 0x7FC00000u;
+            }
+            hi[2 * e] = prmt(x[0], x[1], 0x7632u);
+            hi[2 * e + 1] = prmt(x[2], x[3], 0x7632u);
+            lo[e] = prmt(prmt(x[0], x[1], 0x0051u), prmt(x[2], x[3], 0x0051u), 0x5410u);
           }
-          hi[2 * e] = prmt(x[0], x[1], 0x7632u);
-          hi[2 * e + 1] = prmt(x[2], x[3], 0x7632u);
-          lo[e] = prmt(prmt(x[0], x[1], 0x0051u), prmt(x[2], x[3], 0x0051u), 0x5410u);
+          const uint32_t u = static_cast<uint32_t>(4 * hp + 2 * c);
+          st_cluster_u4(area + u * plane, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+          st_cluster_u4(area + (u + 1u) * plane, make_uint4(hi[4], hi[5], hi[6], hi[7]));
+          st_cluster_u4(area + (8u + (u >> 1)) * plane, make_uint4(lo[0], lo[1], lo[2], lo[3]));
         }
-        const uint32_t row = area + dd * 128u;
-        st_cluster_u4(row + ((2u * hc) ^ (dd & 7u)) * 16u, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-        st_cluster_u4(row + ((2u * hc + 1u) ^ (dd & 7u)) * 16u,
-                      make_uint4(hi[4], hi[5], hi[6], hi[7]));
-        st_cluster_u4(area + off_lo + dd * 64u + (static_cast<uint32_t>(hc) ^ ((dd >> 1) & 3u)) * 16u,
-                      make_uint4(lo[0], lo[1], lo[2], lo[3]));
       }
       if (warp < 2) {
         for (int p = 0; p < S; ++p) {
-          if (p == split) continue;
           st_cluster_f32x2(mapa_shared(recv_slot(split) + off_ml + 8 * tid, static_cast<uint32_t>(p)),
                            m_own, l_own);
         }
@@ -645,73 +677,62 @@ __global__ void __launch_bounds__(kThreads, 1)
       cluster_arrive();  // phase 2: everything is written (release) ...
       cluster_wait();    // ... and visible here (acquire)
       // out = sum_q w_q O_q with w_q = 2^(m_q - M) / L, M = max_q m_q,
-      // L = sum_q 2^(m_q - M) l_q (a range without rows has l_q = 0).
+      // L = sum_q 2^(m_q - M) l_q (a range without rows has l_q = 0). Eight
+      // lanes a head, one for each CTA of the cluster.
       float* wgt = reinterpret_cast<float*>(gbase + kWgt);  // [S][64]
-      if (warp < 2) {
-        auto ml = [&](int q) {  // sender q's (max, sum) of head tid
-          return reinterpret_cast<const float2*>(gbase + (recv_slot(q) - sbase) + off_ml)[tid];
-        };
-        float M = -INFINITY;
+      const int q = lane & 7;
 #pragma unroll 1
-        for (int q = 0; q < S; ++q) {
-          const float2 x = ml(q);
-          if (x.y > 0.f) M = fmaxf(M, x.x);
+      for (int h = 4 * warp + (lane >> 3); h < kHeads; h += kEpiThreads / 8) {
+        float2 x = make_float2(-INFINITY, 0.f);
+        if (q < S) {
+          x = reinterpret_cast<const float2*>(gbase + (recv_slot(q) - sbase) + off_ml)[h];
         }
-        float L = 0.f;
-#pragma unroll 1
-        for (int q = 0; q < S; ++q) {
-          const float2 x = ml(q);
-          const float e = x.y > 0.f ? exp2f(x.x - M) : 0.f;
-          wgt[q * kHeads + tid] = e;
-          L = fmaf(e, x.y, L);
-        }
-        const float inv_L = L > 0.f ? 1.f / L : 0.f;
-#pragma unroll 1
-        for (int q = 0; q < S; ++q) wgt[q * kHeads + tid] *= inv_L;
-        if (a.lse && split == 0) {
-          a.lse[static_cast<int64_t>(b) * kHeads + tid] =
-              L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+        const bool some = !(x.y <= 0.f);  // (a NaN counts)
+        float M = some ? x.x : -INFINITY;
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+        const float e = some ? exp2f(x.x - M) : 0.f;
+        float L = e * x.y;
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, o);
+        if (q < S) wgt[q * kHeads + h] = L == 0.f ? 0.f : e / L;
+        if (a.lse && split == 0 && q == 0) {
+          a.lse[static_cast<int64_t>(b) * kHeads + h] =
+              L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
         }
       }
       named_sync(kEpiBar, kEpiThreads);
       const uint32_t wgt_s = sbase + kWgt;
+      // (8 heads, 32 dims) pairs, in turn over the warps
 #pragma unroll 1
-      for (int i = grp; i < 16; i += kEpiGroups) {
-        const int m = i >> 2, hc = i & 3;
-        const int d = 128 * m + et0 + lane;
-        if (d / D != split) continue;
-        const uint32_t dd = static_cast<uint32_t>(d - split * D);
-        float v[16];
-        load16(m, hc, v);
-        scale16(v, wgt_s + static_cast<uint32_t>(split * kHeads * 4), hc);
-#pragma unroll 1
-        for (int q = 0; q < S; ++q) {
-          if (q == split) continue;
-          const uint32_t area = recv_slot(q);
-          const uint32_t row = area + dd * 128u;
-          const uint4 x0 = ld_shared_v4(row + ((2u * hc) ^ (dd & 7u)) * 16u);
-          const uint4 x1 = ld_shared_v4(row + ((2u * hc + 1u) ^ (dd & 7u)) * 16u);
-          const uint4 y = ld_shared_v4(area + off_lo + dd * 64u +
-                                       (static_cast<uint32_t>(hc) ^ ((dd >> 1) & 3u)) * 16u);
-          const uint32_t hi[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-          const uint32_t lo[4] = {y.x, y.y, y.z, y.w};
-          const uint32_t wq = wgt_s + static_cast<uint32_t>(q * kHeads * 4);
+      for (int i = warp; i < 8 * (D / 32); i += kEpiThreads / 32) {
+        const int u = i & 7, d32 = 32 * (i >> 3);
+        float v[8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float4 w4 = ld_shared_f4(wq + (16 * hc + 4 * e) * 4);
-            // bytes: 0, the 8-bit part, the 16-bit part
+        for (int e = 0; e < 8; ++e) v[e] = 0.f;
+        uint32_t src = sbase + kKV + static_cast<uint32_t>(d32 + lane) * 16u;
+#pragma unroll 2
+        for (int r = 0; r < S; ++r, src += pay) {
+          const uint4 x = ld_shared_v4(src + static_cast<uint32_t>(u) * plane);
+          const uint2 y = ld_shared_v2(src + (8u + (static_cast<uint32_t>(u) >> 1)) * plane +
+                                       8u * (u & 1));
+          const uint32_t hi[4] = {x.x, x.y, x.z, x.w};
+          const uint32_t lo[2] = {y.x, y.y};
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float4 w4 = ld_shared_f4(wgt_s + static_cast<uint32_t>(r * kHeads + 8 * u + 4 * e) * 4);
+            // bytes from the top: the 16-bit part, the 8-bit part, 0
             const uint32_t b01 = hi[2 * e], b23 = hi[2 * e + 1], l4 = lo[e];
-            const float f0 = __uint_as_float(prmt(b01, l4, 0x1040u) & 0xFFFFFF00u);
-            const float f1 = __uint_as_float(prmt(b01, l4, 0x3250u) & 0xFFFFFF00u);
-            const float f2 = __uint_as_float(prmt(b23, l4, 0x1060u) & 0xFFFFFF00u);
-            const float f3 = __uint_as_float(prmt(b23, l4, 0x3270u) & 0xFFFFFF00u);
-            v[4 * e] = fmaf(w4.x, f0, v[4 * e]);
-            v[4 * e + 1] = fmaf(w4.y, f1, v[4 * e + 1]);
-            v[4 * e + 2] = fmaf(w4.z, f2, v[4 * e + 2]);
-            v[4 * e + 3] = fmaf(w4.w, f3, v[4 * e + 3]);
+            v[4 * e] = fmaf(w4.x, __uint_as_float(prmt(b01, l4, 0x1040u) & 0xFFFFFF00u), v[4 * e]);
+            v[4 * e + 1] =
+                fmaf(w4.y, __uint_as_float(prmt(b01, l4, 0x3250u) & 0xFFFFFF00u), v[4 * e + 1]);
+            v[4 * e + 2] =
+                fmaf(w4.z, __uint_as_float(prmt(b23, l4, 0x1060u) & 0xFFFFFF00u), v[4 * e + 2]);
+            v[4 * e + 3] =
+                fmaf(w4.w, __uint_as_float(prmt(b23, l4, 0x3270u) & 0xFFFFFF00u), v[4 * e + 3]);
           }
         }
-        store_heads16(out, 16 * hc, 128 * m + et0, lane, v);
+        store_heads8(out, 8 * u, split * D + d32, lane, v);
       }
     }
   }
