@@ -7,7 +7,7 @@
 //   O^T += KV^T . P^T (four M = 128 slices of the 512 latent dims, N = 64 heads,
 //                      K = 64 rows; the KV tile is read as an MN-major operand)
 //
-// A row is 272 bytes, so a CTA's rows fit in registers on their way: eight
+// A row is 272 bytes, so a tile's rows fit in registers on their way: eight
 // loader warps read a tile's codes (16 bytes a lane: 32 elements, one scale)
 // while they convert the tile before it to bf16 into a swizzled operand slot.
 // bf16 holds every code times every scale exactly, so Q stays as it is given
@@ -55,14 +55,15 @@ constexpr int kAtomBytes = kRows * 128;            // 64 dims of a tile's rows
 constexpr int kSlotBytes = 8 * kAtomBytes;
 constexpr int kQ = 0;                              // 8 atoms x 64 heads x 128 B
 constexpr uint32_t kQBytes = kHeads * kLatent * 2;
-constexpr int kP = kQ + static_cast<int>(kQBytes); // 2 x (64 heads x 64 rows bf16)
+constexpr int kP = kQ + static_cast<int>(kQBytes); // 64 heads x 64 rows bf16
 constexpr int kPBytes = kHeads * 128;
-constexpr int kKV = kP + 2 * kPBytes;              // the two slots
+constexpr int kKV = kP + kPBytes;                  // the two slots
 constexpr int kKVBytes = kSlots * kSlotBytes;
 constexpr int kIds = kKV + kKVBytes;               // compacted latent rows
 constexpr int kMisc = kIds + kMaxKTokens * 4;
 constexpr int kMiscBytes = 2048;
 constexpr int kSmemBytes = kMisc + kMiscBytes + 1024;  // + alignment slack of the base
+static_assert(kSmemBytes <= 227 * 1024 && kIds % 16 == 0 && kMisc % 16 == 0, "shared memory");
 constexpr int kTmemCols = 512;  // S[b]: cols [32 b, 32 b + 32); O^T slice m: [kTmemO + 64 m, ...)
 constexpr int kTmemO = 64;
 
@@ -76,11 +77,11 @@ __host__ __device__ constexpr int xchg_bytes(int S) { return xchg_ml(S) + kHeads
 static_assert(2 * xchg_bytes(2) <= kKVBytes && 4 * xchg_bytes(4) <= kKVBytes &&
                   kMaxAttnSplits * xchg_bytes(kMaxAttnSplits) <= kKVBytes,
               "receive areas fit the slots");
-constexpr int kWgt = kP;  // [S][64] merge weights, in the P buffers
-static_assert(kMaxAttnSplits * kHeads * 4 <= 2 * kPBytes, "merge weights fit the P buffers");
+constexpr int kWgt = kP;  // [S][64] merge weights, in the P buffer
+static_assert(kMaxAttnSplits * kHeads * 4 <= kPBytes, "merge weights fit the P buffer");
 
 struct Misc {
-  uint64_t kv_full[kSlots], kv_empty[kSlots], s_full[2], s_free[2], p_full[2], p_empty[2];
+  uint64_t kv_full[kSlots], kv_empty[kSlots], s_full[2], s_free[2], p_full, p_empty;
   uint64_t q_done, ids_ready;
   uint64_t o_done;  // every MMA of the CTA has completed
   uint32_t tmem_base;
@@ -95,44 +96,61 @@ static_assert(sizeof(Misc) <= kMiscBytes, "misc block");
 
 // A converged warp's bounded wait; every lane gets the same answer (a lane whose
 // wait ran out takes the warp with it), so that warp-wide instructions after it
-// stay converged.
+// stay converged. The loop is kept out of line: the roles' code runs from a small
+// instruction cache, and inlined at every wait it was a large part of it.
+__device__ __noinline__ bool wait_loop(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                       DeviceStatus* st) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait_abortable(bar, parity, abort, st, SITE_ATTN));
+}
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Misc* m,
                                          DeviceStatus* st) {
-  return __all_sync(0xFFFFFFFFu, mbar_wait_abortable(bar, parity, &m->abort, st, SITE_ATTN));
+  if (__all_sync(0xFFFFFFFFu, mbar_try_wait(smem_u32(bar), parity))) return true;
+  return wait_loop(bar, parity, &m->abort, st);
 }
 
-// MMAs and commits of a converged warp, issued by one elected lane (the same
-// lane each time): the operands stay in uniform registers.
-__device__ __forceinline__ void mma_f16_warp(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                             uint32_t idesc, uint32_t accumulate) {
+// MMAs and commits of a converged warp, issued by its leader (elect_leader, the
+// same lane each time). A descriptor's upper half is constant and the lower one
+// holds the address (16-byte units; every operand lies below 256 KB, so adding to it
+// does not carry).
+__device__ __forceinline__ uint32_t elect_leader() {
+  uint32_t r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r));
+  return r;
 }
-__device__ __forceinline__ void mma_ws_f16_warp(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                                uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
-      " @q tcgen05.mma.ws.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
+template <bool WS>
+__device__ __forceinline__ void mma_warp(uint32_t leader, uint32_t d_tmem, uint32_t a_lo,
+                                         uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                         uint32_t idesc, uint32_t accumulate) {
+  if constexpr (WS) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n .reg .b64 x, y;\n setp.ne.b32 q, %0, 0;\n setp.ne.b32 p, %7, 0;\n"
+        " mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
+        " @q tcgen05.mma.ws.cta_group::1.kind::f16 [%1], x, y, %6, p;\n}\n" ::"r"(leader),
+        "r"(d_tmem), "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n .reg .pred p, q;\n .reg .b64 x, y;\n setp.ne.b32 q, %0, 0;\n setp.ne.b32 p, %7, 0;\n"
+        " mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%1], x, y, %6, p;\n}\n" ::"r"(leader),
+        "r"(d_tmem), "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+        : "memory");
+  }
 }
-__device__ __forceinline__ void mma_commit_warp(uint64_t* bar) {
+__device__ __forceinline__ void mma_commit_warp(uint32_t leader, uint64_t* bar) {
   asm volatile(
-      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
-      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
-          smem_u32(bar))
+      "{\n .reg .pred q;\n setp.ne.b32 q, %0, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n}\n" ::"r"(
+          leader),
+      "r"(smem_u32(bar))
       : "memory");
 }
 
-// A loader lane's part of a tile: 16 bytes of codes and their scale byte of
-// four rows.
-struct Codes {
-  uint4 c[kWarpRows / 2];
-  uint32_t s[kWarpRows / 2];
-};
+__device__ __noinline__ void report(DeviceStatus* st, uint32_t detail) {
+  record_status(st, DSA_ERR_DEVICE_CHECK, SITE_ATTN, detail);
+}
 
 // out[h0 + i][d] = v[i] for 8 heads, lane l holding dim d = d32 + l of a
 // 32-aligned range: three exchanges with lanes 1, 2 and 4 away leave each lane
@@ -179,6 +197,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int split = blockIdx.y;  // rank in the cluster
   const int S = a.splits;
   const bool paired = S > 1;
+  int n_vis = a.n_latents[b];
+  int n_sw = a.swa_len[b];
 
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
@@ -188,9 +208,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&misc->s_full[i], 1);
       mbar_init(&misc->s_free[i], 4);
-      mbar_init(&misc->p_full[i], 4);
-      mbar_init(&misc->p_empty[i], 1);
     }
+    mbar_init(&misc->p_full, 4);
+    mbar_init(&misc->p_empty, 1);
     mbar_init(&misc->q_done, 1);     // the TMA loads of Q (expect-tx arrival + 64 KB)
     mbar_init(&misc->ids_ready, 1);  // the math warps compacted the token ids
     mbar_init(&misc->o_done, 1);     // the PV issuer's last commit
@@ -206,10 +226,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // thread arrives here and waits before its first cluster access.
   if (paired) cluster_arrive_relaxed();
 
-  int n_vis = a.n_latents[b];
-  int n_sw = a.swa_len[b];
   if (n_sw < 0 || n_sw > a.window) {
-    if (tid == 0 && split == 0) record_status(a.status, DSA_ERR_DEVICE_CHECK, SITE_ATTN, b);
+    if (tid == 0 && split == 0) report(a.status, static_cast<uint32_t>(b));
     n_sw = n_sw < 0 ? 0 : a.window;
   }
   if (n_vis > a.lat_stride) n_vis = static_cast<int>(a.lat_stride);
@@ -255,16 +273,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (i < a.k_tokens) {
         id = tk[i];
         if (id >= n_vis) {
-          if (split == 0) {
-            record_status(a.status, DSA_ERR_DEVICE_CHECK, SITE_ATTN, static_cast<uint32_t>(id));
-          }
+          if (split == 0) report(a.status, static_cast<uint32_t>(id));
           id = -1;
         }
         if (paged && id >= 0) {
           const int64_t row = paged_row(a.pages, b, id);
-          if (row < 0 && split == 0) {
-            record_status(a.status, DSA_ERR_DEVICE_CHECK, SITE_ATTN, static_cast<uint32_t>(id));
-          }
+          if (row < 0 && split == 0) report(a.status, static_cast<uint32_t>(id));
           id = static_cast<int>(row);
         }
       }
@@ -300,84 +314,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- loaders ----------------
     // Loader warp w fills rows [8 w, 8 w + 8) of every tile, two rows at a
     // time: lane l reads bytes [16 j, 16 j + 16) of row 8 w + 2 i + l / 16,
-    // j = l % 16, which are its elements [32 j, 32 j + 32) under scale j. A
-    // tile's codes wait in registers (two sets) while the tile before is
-    // converted; rows without a source are zeros.
+    // j = l % 16, which are its elements [32 j, 32 j + 32) under scale j. As soon as
+    // a pair of rows is converted, the same pair of the next tile is read into the
+    // same registers, so a tile's reads have the time of a tile to arrive. One copy
+    // of the code does every pass (the first only reads, the last only converts).
+    // Rows without a source are zeros.
     const int w = warp - kLoadWarp0;
     const int j = lane & 15, half = lane >> 4;
     const uint8_t* lat = reinterpret_cast<const uint8_t*>(a.latents);
     const uint8_t* swa = reinterpret_cast<const uint8_t*>(a.swa);
     bool have_ids = false;
     int s_begin = 0, n_rows_cta = w_cnt, n_tiles = 0;
-    Codes cur, nxt;
-    auto load = [&](int t, Codes& k) {
-      // Lane r < 8 finds the source of row 8 w + r of the tile: its byte
-      // offset, or -1; bit 62 marks the window.
-      int64_t src_l = -1;
-      const int g = t * kRows + kWarpRows * w + lane;
-      if (lane < kWarpRows && g < n_rows_cta) {
-        if (g < w_cnt) {
-          const int64_t row = wrow0 + w_begin + g;
-          if (DSA_DCHECK(row >= 0 && row < a.swa_rows, a.status, SITE_ATTN, row)) {
-            src_l = row * kRow4Bytes | (int64_t{1} << 62);
-          }
-        } else {
-          const int64_t row = lat_row0 + ids[s_begin + g - w_cnt];
-          if (DSA_DCHECK(row >= 0 && row < a.lat_rows, a.status, SITE_ATTN, row)) {
-            src_l = row * kRow4Bytes;
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kWarpRows / 2; ++i) {
-        const int64_t src = __shfl_sync(0xFFFFFFFFu, src_l, 2 * i + half);
-        k.c[i] = make_uint4(0u, 0u, 0u, 0u);
-        k.s[i] = 0u;
-        if (src >= 0) {
-          const uint8_t* p = (src >> 62 ? swa : lat) + (src & ~(int64_t{1} << 62));
-          k.c[i] = __ldg(reinterpret_cast<const uint4*>(p) + j);
-          k.s[i] = __ldg(p + kRow4Codes + j);
-        }
-      }
-    };
-    auto store = [&](int t, const Codes& k) -> bool {
-      const int sl = t % kSlots;
-      if (t >= kSlots && !wait_bar(&misc->kv_empty[sl],
-                                   static_cast<uint32_t>(((t / kSlots) - 1) & 1), misc, a.status)) {
-        return false;
-      }
-      // Word i of the 16 bytes is 16-byte chunk 4 (j & 1) + i of the row in
-      // atom j / 2. The order is rotated by atom so that eight lanes (four
-      // atoms, both halves) write eight different 16-byte bank groups.
-      const int rot = (j >> 1) & 3;
-      const uint32_t base = sbase + kKV + sl * kSlotBytes +
-                            static_cast<uint32_t>(j >> 1) * kAtomBytes;
-#pragma unroll
-      for (int i = 0; i < kWarpRows / 2; ++i) {
-        uint4 c = k.c[i];
-        if (rot & 1) c = make_uint4(c.y, c.z, c.w, c.x);
-        if (rot & 2) c = make_uint4(c.z, c.w, c.x, c.y);
-        const uint32_t f = mx4_scale_bf16x2(k.s[i]);
-        const uint32_t row = static_cast<uint32_t>(kWarpRows * w + 2 * i + half);
-        const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const uint32_t chunk = 4u * (j & 1) + ((n + rot) & 3);
-          st_shared_v4(base + sw128_off(row, chunk), mx4_decode8(cw[n], f));
-        }
-      }
-      fence_proxy_async_smem();  // the MMAs read the tile through the async proxy
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&misc->kv_full[sl]);
-      return true;
-    };
-    // Tile `stored` (in cur) is converted once tile `stored + 1` (in nxt) is on its way;
-    // when the next tile waits for the ids, the one at hand is converted first.
-    int loaded = 0, stored = 0;  // tiles read, tiles converted
-    while (ok) {
-      if (!have_ids && (loaded + 1) * kRows > w_cnt &&
-          (loaded == stored ||
-           __all_sync(0xFFFFFFFFu, mbar_try_wait(smem_u32(&misc->ids_ready), 0u)))) {
+    uint4 code[kWarpRows / 2];
+    uint32_t scale[kWarpRows / 2];
+    int next = 0, done = 0;  // tiles read, tiles converted
+    for (;;) {
+      const bool conv = next > done;
+      // The next tile is read in this pass, unless that needs ids that are not there
+      // yet while a tile is at hand (the conversion then goes first).
+      bool read = !have_ids && (next + 1) * kRows <= w_cnt;
+      if (!have_ids && !read &&
+          (!conv || __all_sync(0xFFFFFFFFu, mbar_try_wait(smem_u32(&misc->ids_ready), 0u)))) {
         if (!wait_bar(&misc->ids_ready, 0u, misc, a.status)) {
           ok = false;
           break;
@@ -388,16 +345,73 @@ __global__ void __launch_bounds__(kThreads, 1)
         n_tiles = (n_rows_cta + kRows - 1) / kRows;
         have_ids = true;
       }
-      const bool more = have_ids ? loaded < n_tiles : (loaded + 1) * kRows <= w_cnt;
-      if (loaded == stored) {
-        if (!more) break;
-        load(loaded++, cur);
-        continue;
+      if (have_ids) read = next < n_tiles;
+      if (!conv && !read) break;
+      // Lane r < 8 finds the source of row 8 w + r: its byte offset, or -1; bit 62
+      // marks the window.
+      int64_t src_l = -1;
+      if (read) {
+        const int g = next * kRows + kWarpRows * w + lane;
+        if (lane < kWarpRows && g < n_rows_cta) {
+          if (g < w_cnt) {
+            const int64_t row = wrow0 + w_begin + g;
+            if (DSA_DCHECK(row >= 0 && row < a.swa_rows, a.status, SITE_ATTN, row)) {
+              src_l = row * kRow4Bytes | (int64_t{1} << 62);
+            }
+          } else {
+            const int64_t row = lat_row0 + ids[s_begin + g - w_cnt];
+            if (DSA_DCHECK(row >= 0 && row < a.lat_rows, a.status, SITE_ATTN, row)) {
+              src_l = row * kRow4Bytes;
+            }
+          }
+        }
       }
-      const bool ahead = more && loaded == stored + 1;
-      if (ahead) load(loaded++, nxt);
-      if (!store(stored++, cur)) ok = false;
-      if (ahead) cur = nxt;
+      const int sl = done % kSlots;
+      if (conv && done >= kSlots &&
+          !wait_bar(&misc->kv_empty[sl], static_cast<uint32_t>(((done / kSlots) - 1) & 1), misc,
+                    a.status)) {
+        ok = false;
+        break;
+      }
+      // Word i of the 16 bytes is 16-byte chunk 4 (j & 1) + i of the row in
+      // atom j / 2. The order is rotated by atom so that eight lanes (four
+      // atoms, both halves) write eight different 16-byte bank groups.
+      const int rot = (j >> 1) & 3;
+      const uint32_t base = sbase + kKV + sl * kSlotBytes +
+                            static_cast<uint32_t>(j >> 1) * kAtomBytes;
+#pragma unroll
+      for (int i = 0; i < kWarpRows / 2; ++i) {
+        if (conv) {
+          uint4 c = code[i];
+          if (rot & 1) c = make_uint4(c.y, c.z, c.w, c.x);
+          if (rot & 2) c = make_uint4(c.z, c.w, c.x, c.y);
+          const uint32_t f = mx4_scale_bf16x2(scale[i]);
+          const uint32_t row = static_cast<uint32_t>(kWarpRows * w + 2 * i + half);
+          const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            const uint32_t chunk = 4u * (j & 1) + ((n + rot) & 3);
+            st_shared_v4(base + sw128_off(row, chunk), mx4_decode8(cw[n], f));
+          }
+        }
+        if (read) {
+          const int64_t src = __shfl_sync(0xFFFFFFFFu, src_l, 2 * i + half);
+          code[i] = make_uint4(0u, 0u, 0u, 0u);
+          scale[i] = 0u;
+          if (src >= 0) {
+            const uint8_t* p = (src >> 62 ? swa : lat) + (src & ~(int64_t{1} << 62));
+            code[i] = __ldg(reinterpret_cast<const uint4*>(p) + j);
+            scale[i] = __ldg(p + kRow4Codes + j);
+          }
+        }
+      }
+      if (conv) {
+        fence_proxy_async_smem();  // the MMAs read the tile through the async proxy
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&misc->kv_full[sl]);
+        ++done;
+      }
+      if (read) ++next;
     }
     n_tiles_e = have_ids ? n_tiles : 0;
   } else if (warp == kMmaWarp || warp == kPvWarp) {
@@ -411,32 +425,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     // PV(t) is issued only after the softmax of tile t, hence after QK^T(t)
     // completed: its commit alone frees the tile's slot, and the PV issuer's
     // last commit means every MMA of the CTA has completed.
+    const uint32_t leader = elect_leader();
+    const uint64_t kv_mn = sw128_desc(sbase + kKV, kAtomBytes, 1024);  // slot 0, MN-major
+    const uint64_t kv_k = sw128_desc(sbase + kKV, 16, 1024);           // slot 0, K-major
+    const uint64_t q_k = sw128_desc(sbase + kQ, 16, 1024);
+    const uint64_t p_k = sw128_desc(sbase + kP, 16, 1024);
+    auto lo = [](uint64_t d) { return static_cast<uint32_t>(d); };
+    auto hi = [](uint64_t d) { return static_cast<uint32_t>(d >> 32); };
     if (warp == kPvWarp) {
       constexpr uint32_t idesc_o = mma_idesc(128, kHeads, true, true, false);
       for (int t = 0; t < n_tiles; ++t) {
-        const int sb = t & 1, sl = t % kSlots;
-        if (!wait_bar(&misc->p_full[sb], static_cast<uint32_t>((t >> 1) & 1), misc, a.status)) {
-          break;
-        }
+        const int sl = t % kSlots;
+        if (!wait_bar(&misc->p_full, static_cast<uint32_t>(t & 1), misc, a.status)) break;
         tc_fence_after();
         fence_proxy_async_smem();
-        // Descriptors are built once and stepped by their start-address field
-        // (16-byte units; every operand lies below 256 KB, so no carry).
-        const uint64_t ad0 = sw128_desc(sbase + kKV + sl * kSlotBytes, kAtomBytes, 1024);
-        const uint64_t bd0 = sw128_desc(sbase + kP + sb * kPBytes, 16, 1024);
-#pragma unroll
+        uint32_t a_lo = lo(kv_mn) + static_cast<uint32_t>(sl * kSlotBytes >> 4);
+#pragma unroll 1
         for (int m = 0; m < 4; ++m) {
 #pragma unroll
           for (int ks = 0; ks < kRows / 16; ++ks) {
-            const uint64_t ad = ad0 + ((m * 2 * kAtomBytes + ks * 16 * 128) >> 4);
-            const uint64_t bd = bd0 + ((ks * 32) >> 4);
-            mma_f16_warp(tmem + kTmemO + 64 * m, ad, bd, idesc_o, (t > 0 || ks > 0) ? 1u : 0u);
+            mma_warp<false>(leader, tmem + kTmemO + 64 * m, a_lo + ((ks * 16 * 128) >> 4), hi(kv_mn),
+                            lo(p_k) + ((ks * 32) >> 4), hi(p_k), idesc_o,
+                            (t > 0 || ks > 0) ? 1u : 0u);
           }
+          a_lo += (2 * kAtomBytes) >> 4;
         }
-        mma_commit_warp(&misc->kv_empty[sl]);
-        mma_commit_warp(&misc->p_empty[sb]);
+        mma_commit_warp(leader, &misc->kv_empty[sl]);
+        mma_commit_warp(leader, &misc->p_empty);
       }
-      if (n_tiles > 0) mma_commit_warp(&misc->o_done);  // arrives once every MMA has completed
+      if (n_tiles > 0) mma_commit_warp(leader, &misc->o_done);  // every MMA has completed
     } else {
       constexpr uint32_t idesc_s = mma_idesc(kHeads, kRows, true, false, false);
       bool qk_ok = n_tiles == 0 || wait_bar(&misc->q_done, 0u, misc, a.status);
@@ -451,15 +468,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         fence_proxy_async_smem();
-        const uint64_t ad0 = sw128_desc(sbase + kQ, 16, 1024);
-        const uint64_t bd0 = sw128_desc(sbase + kKV + sl * kSlotBytes, 16, 1024);
+        uint32_t a_lo = lo(q_k), b_lo = lo(kv_k) + static_cast<uint32_t>(sl * kSlotBytes >> 4);
+#pragma unroll 1
+        for (int c = 0; c < kLatent / 64; ++c) {  // atoms of 64 dims
 #pragma unroll
-        for (int ks = 0; ks < kLatent / 16; ++ks) {
-          const uint64_t ad = ad0 + (((ks >> 2) * (kHeads * 128) + (ks & 3) * 32) >> 4);
-          const uint64_t bd = bd0 + (((ks >> 2) * kAtomBytes + (ks & 3) * 32) >> 4);
-          mma_ws_f16_warp(tmem + 32 * sb, ad, bd, idesc_s, ks > 0 ? 1u : 0u);
+          for (int ks = 0; ks < 4; ++ks) {
+            mma_warp<true>(leader, tmem + 32 * sb, a_lo + ((ks * 32) >> 4), hi(q_k),
+                           b_lo + ((ks * 32) >> 4), hi(kv_k), idesc_s, (c > 0 || ks > 0) ? 1u : 0u);
+          }
+          a_lo += (kHeads * 128) >> 4;
+          b_lo += kAtomBytes >> 4;
         }
-        mma_commit_warp(&misc->s_full[sb]);
+        mma_commit_warp(leader, &misc->s_full[sb]);
       }
     }
     __syncwarp();
@@ -484,12 +504,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t la = tmem_addr(tmem, static_cast<uint32_t>(32 * warp), 0);
     const int half = warp >> 1, h = tid & (kHeads - 1);
     const float sl = a.scale_log2;
-    // PV(j) is known complete through p_empty[j & 1], whose phases a thread
-    // consumes in order (at most one phase ahead of its last wait).
+    // PV(t) is known complete through p_empty's phase t; a thread waits for every phase
+    // in turn, so a parity wait is never more than one phase off.
     auto wait_pv = [&](int t) {
-      if (ok) {
-        ok = wait_bar(&misc->p_empty[t & 1], static_cast<uint32_t>((t >> 1) & 1), misc, a.status);
-      }
+      if (ok) ok = wait_bar(&misc->p_empty, static_cast<uint32_t>(t & 1), misc, a.status);
     };
     constexpr int kHalf = kRows / 2;
     for (int t = 0; t < n_tiles; ++t) {
@@ -543,13 +561,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           named_sync(kMathBar, 128);  // alpha is read by all before the next tile rewrites it
         }
       }
-      if (t >= 2) wait_pv(t - 2);  // P[sb] was last read by PV(t - 2)
+      if (t >= 1) wait_pv(t - 1);  // P was last read by PV(t - 1)
       if (ok) {
         uint32_t pk[kHalf / 2];
         // the denominator sums the fp32 probabilities; the MMA takes them in
         // bf16, the type of its other operand
         l_run = l_run * alpha + exp_pack<kHalf>(z, sl, m_run, pk);
-        const uint32_t pb = sbase + kP + sb * kPBytes;
+        const uint32_t pb = sbase + kP;
 #pragma unroll
         for (int c = 0; c < kHalf / 8; ++c) {
           st_shared_v4(pb + sw128_off(h, 4 * half + c),
@@ -558,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&misc->p_full[sb]);
+      if (lane == 0) mbar_arrive(&misc->p_full);
     }
     // the two halves' sums (the order is fixed)
     if (half == 1) misc->mx[0][0][h] = l_run;
@@ -625,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // CTA `split` finishes dims [split D, split D + D). Each CTA writes its part for
       // each CTA straight into that one's receive area (its slots, free once its MMAs
       // are done). A warp's 32 dims always go to one CTA.
-      const int D = kLatent / S;
+      const int D = kLatent / S, lg_d = 31 - __clz(D);
       const uint32_t pay = static_cast<uint32_t>(xchg_bytes(S));
       const uint32_t off_ml = static_cast<uint32_t>(xchg_ml(S));
       const uint32_t plane = static_cast<uint32_t>(D) * 16u;
@@ -640,9 +658,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = grp; i < 8; i += kEpiGroups) {
         const int m = i >> 1, hp = i & 1;
         const int d = 128 * m + et0 + lane;
-        const int p = d / D;
-        const uint32_t area = mapa_shared(recv_slot(split), static_cast<uint32_t>(p)) +
-                              static_cast<uint32_t>(d - p * D) * 16u;
+        const int p = d >> lg_d;
+        const uint32_t mine = recv_slot(split) + static_cast<uint32_t>(d - p * D) * 16u;
+        const uint32_t area = mapa_shared(mine, static_cast<uint32_t>(p));
         float v[32];
         load32(m, hp, v);
 #pragma unroll
@@ -663,9 +681,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             lo[e] = prmt(prmt(x[0], x[1], 0x0051u), prmt(x[2], x[3], 0x0051u), 0x5410u);
           }
           const uint32_t u = static_cast<uint32_t>(4 * hp + 2 * c);
-          st_cluster_u4(area + u * plane, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-          st_cluster_u4(area + (u + 1u) * plane, make_uint4(hi[4], hi[5], hi[6], hi[7]));
-          st_cluster_u4(area + (8u + (u >> 1)) * plane, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+          const uint4 h0 = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          const uint4 h1 = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+          const uint4 l0 = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          if (p == split) {  // its own part, by plain stores
+            st_shared_v4(mine + u * plane, h0);
+            st_shared_v4(mine + (u + 1u) * plane, h1);
+            st_shared_v4(mine + (8u + (u >> 1)) * plane, l0);
+          } else {
+            st_cluster_u4(area + u * plane, h0);
+            st_cluster_u4(area + (u + 1u) * plane, h1);
+            st_cluster_u4(area + (8u + (u >> 1)) * plane, l0);
+          }
         }
       }
       if (warp < 2) {
@@ -703,24 +730,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       named_sync(kEpiBar, kEpiThreads);
       const uint32_t wgt_s = sbase + kWgt;
-      // (8 heads, 32 dims) pairs, in turn over the warps
+      // (16 heads, 32 dims) pairs, in turn over the warps
 #pragma unroll 1
-      for (int i = warp; i < 8 * (D / 32); i += kEpiThreads / 32) {
-        const int u = i & 7, d32 = 32 * (i >> 3);
-        float v[8];
+      for (int i = warp; i < 4 * (D / 32); i += kEpiThreads / 32) {
+        const uint32_t g = static_cast<uint32_t>(i & 3);
+        const int d32 = 32 * (i >> 2);
+        float v[16];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = 0.f;
+        for (int e = 0; e < 16; ++e) v[e] = 0.f;
         uint32_t src = sbase + kKV + static_cast<uint32_t>(d32 + lane) * 16u;
 #pragma unroll 2
         for (int r = 0; r < S; ++r, src += pay) {
-          const uint4 x = ld_shared_v4(src + static_cast<uint32_t>(u) * plane);
-          const uint2 y = ld_shared_v2(src + (8u + (static_cast<uint32_t>(u) >> 1)) * plane +
-                                       8u * (u & 1));
-          const uint32_t hi[4] = {x.x, x.y, x.z, x.w};
-          const uint32_t lo[2] = {y.x, y.y};
+          const uint4 x0 = ld_shared_v4(src + 2u * g * plane);
+          const uint4 x1 = ld_shared_v4(src + (2u * g + 1u) * plane);
+          const uint4 y = ld_shared_v4(src + (8u + g) * plane);
+          const uint32_t hi[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+          const uint32_t lo[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float4 w4 = ld_shared_f4(wgt_s + static_cast<uint32_t>(r * kHeads + 8 * u + 4 * e) * 4);
+          for (int e = 0; e < 4; ++e) {
+            const float4 w4 =
+                ld_shared_f4(wgt_s + (static_cast<uint32_t>(r) * kHeads + 16u * g + 4u * e) * 4u);
             // bytes from the top: the 16-bit part, the 8-bit part, 0
             const uint32_t b01 = hi[2 * e], b23 = hi[2 * e + 1], l4 = lo[e];
             v[4 * e] = fmaf(w4.x, __uint_as_float(prmt(b01, l4, 0x1040u) & 0xFFFFFF00u), v[4 * e]);
@@ -732,7 +761,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fmaf(w4.w, __uint_as_float(prmt(b23, l4, 0x3270u) & 0xFFFFFF00u), v[4 * e + 3]);
           }
         }
-        store_heads8(out, 8 * u, split * D + d32, lane, v);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float o[8] = {v[8 * c],     v[8 * c + 1], v[8 * c + 2], v[8 * c + 3],
+                              v[8 * c + 4], v[8 * c + 5], v[8 * c + 6], v[8 * c + 7]};
+          store_heads8(out, 16 * static_cast<int>(g) + 8 * c, split * D + d32, lane, o);
+        }
       }
     }
   }
