@@ -23,10 +23,11 @@
 // share the softmax.
 //
 // The split over a cluster of S CTAs, the lazy softmax maximum and the roles
-// are those of the attention over bf16 rows. The partial outputs that the CTAs
-// of a cluster exchange keep 24 bits of their fp32 value (sign, exponent, 15
-// mantissa bits), as a 16-bit and an 8-bit part: with bf16 parts their rounding
-// would add to the output's own, which is of the same size.
+// are those of the attention over bf16 rows. The CTAs of a cluster exchange their
+// (max, sum) first, so each scales its partial output by its final weight and the
+// merge is a sum. The partial outputs keep the upper 24 bits of their fp32 value
+// (sign, exponent, 15 mantissa bits), as a 16-bit and an 8-bit part: with bf16 parts
+// their rounding would add to the output's own, which is of the same size.
 #include <algorithm>
 #include <cstddef>
 
@@ -60,7 +61,8 @@ constexpr int kPBytes = kHeads * 128;
 constexpr int kKV = kP + kPBytes;                  // the two slots
 constexpr int kKVBytes = kSlots * kSlotBytes;
 constexpr int kIds = kKV + kKVBytes;               // compacted latent rows
-constexpr int kMisc = kIds + kMaxKTokens * 4;
+constexpr int kMl = kIds + kMaxKTokens * 4;        // [8][64] (max, sum) of each CTA's rows
+constexpr int kMisc = kMl + kMaxAttnSplits * kHeads * 8;
 constexpr int kMiscBytes = 2048;
 constexpr int kSmemBytes = kMisc + kMiscBytes + 1024;  // + alignment slack of the base
 static_assert(kSmemBytes <= 227 * 1024 && kIds % 16 == 0 && kMisc % 16 == 0, "shared memory");
@@ -68,17 +70,13 @@ constexpr int kTmemCols = 512;  // S[b]: cols [32 b, 32 b + 32); O^T slice m: [k
 constexpr int kTmemO = 64;
 
 // What a CTA gives the one finishing dims [p D, p D + D), D = 512 / S (itself
-// included): its unnormalised O for those dims, then its (max, sum) per head.
-// O lies in planes of D x 16 bytes: plane u < 8 the upper 16 bits of heads
+// included): its part of the output for those dims, in planes of D x 16 bytes: plane u < 8 the upper 16 bits of heads
 // 8 u .. 8 u + 7 for each dim, plane 8 + u the next 8 bits of heads 16 u ..
 // 16 u + 15, so that a warp (32 dims) writes and reads 512 contiguous bytes.
-__host__ __device__ constexpr int xchg_ml(int S) { return (kLatent / S) * 192; }
-__host__ __device__ constexpr int xchg_bytes(int S) { return xchg_ml(S) + kHeads * 8; }
+__host__ __device__ constexpr int xchg_bytes(int S) { return (kLatent / S) * 192; }
 static_assert(2 * xchg_bytes(2) <= kKVBytes && 4 * xchg_bytes(4) <= kKVBytes &&
                   kMaxAttnSplits * xchg_bytes(kMaxAttnSplits) <= kKVBytes,
               "receive areas fit the slots");
-constexpr int kWgt = kP;  // [S][64] merge weights, in the P buffer
-static_assert(kMaxAttnSplits * kHeads * 4 <= kPBytes, "merge weights fit the P buffer");
 
 struct Misc {
   uint64_t kv_full[kSlots], kv_empty[kSlots], s_full[2], s_free[2], p_full, p_empty;
@@ -90,7 +88,7 @@ struct Misc {
   int warp_cnt[4];
   float mx[2][2][kHeads];  // a tile's largest score of each head in rows 0..31 and 32..63
   alignas(16) float alpha[kHeads];
-  alignas(16) float inv_l[kHeads];
+  alignas(16) float wgt[kHeads];  // what a head's O is scaled by
 };
 static_assert(sizeof(Misc) <= kMiscBytes, "misc block");
 
@@ -152,36 +150,50 @@ __device__ __noinline__ void report(DeviceStatus* st, uint32_t detail) {
   record_status(st, DSA_ERR_DEVICE_CHECK, SITE_ATTN, detail);
 }
 
-// out[h0 + i][d] = v[i] for 8 heads, lane l holding dim d = d32 + l of a
+// out[h0 + i][d] = v[i] for NH heads, lane l holding dim d = d32 + l of a
 // 32-aligned range: three exchanges with lanes 1, 2 and 4 away leave each lane
-// 8 consecutive dims of one head, so a warp writes 64 contiguous bytes of each of
-// eight heads by one 16-byte store a lane (2-byte stores, one head at a time,
+// 8 consecutive dims of one head in eight, so a warp writes 64 contiguous bytes of each
+// of eight heads by one 16-byte store a lane (2-byte stores, one head at a time,
 // take eight times as many).
-__device__ __forceinline__ void store_heads8(uint16_t* out, int h0, int d32, int lane,
-                                             const float (&v)[8]) {
+template <int NH>
+__device__ __forceinline__ void store_heads(uint16_t* out, int h0, int d32, int lane,
+                                            const float (&v)[NH]) {
   const bool b0 = lane & 1, b1 = lane & 2, b2 = lane & 4;
-  uint32_t r[4];
+  uint32_t r[NH / 2];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {  // r[j]: head 2 j + b0, two dims
+  for (int j = 0; j < NH / 2; ++j) {  // head 2 j + b0, two dims
     const __nv_bfloat162 x = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-    const uint32_t own = *reinterpret_cast<const uint32_t*>(&x);
-    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
-    r[j] = b0 ? prmt(got, own, 0x7632u) : prmt(own, got, 0x5410u);
+    r[j] = *reinterpret_cast<const uint32_t*>(&x);
   }
-  uint2 u[2];
+  uint32_t g[NH / 2];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {  // u[j]: head 4 j + 2 b1 + b0, four dims
-    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, b1 ? r[2 * j] : r[2 * j + 1], 2);
-    u[j] = b1 ? make_uint2(got, r[2 * j + 1]) : make_uint2(r[2 * j], got);
+  for (int j = 0; j < NH / 2; ++j) g[j] = __shfl_xor_sync(0xFFFFFFFFu, r[j], 1);
+  const uint32_t sel = b0 ? 0x3276u : 0x5410u;
+#pragma unroll
+  for (int j = 0; j < NH / 2; ++j) r[j] = prmt(r[j], g[j], sel);
+#pragma unroll
+  for (int j = 0; j < NH / 4; ++j) {  // head 4 j + 2 b1 + b0, four dims
+    g[j] = __shfl_xor_sync(0xFFFFFFFFu, b1 ? r[2 * j] : r[2 * j + 1], 2);
   }
-  // head 4 b2 + 2 b1 + b0, eight dims
-  const uint2 send = b2 ? u[0] : u[1];
-  const uint2 got = make_uint2(__shfl_xor_sync(0xFFFFFFFFu, send.x, 4),
-                               __shfl_xor_sync(0xFFFFFFFFu, send.y, 4));
-  const uint4 w = b2 ? make_uint4(got.x, got.y, u[1].x, u[1].y)
-                     : make_uint4(u[0].x, u[0].y, got.x, got.y);
-  *reinterpret_cast<uint4*>(out + static_cast<int64_t>(h0 + (lane & 7)) * kLatent + d32 +
-                            (lane & 24)) = w;
+  uint2 u[NH / 4];
+#pragma unroll
+  for (int j = 0; j < NH / 4; ++j) {
+    u[j] = b1 ? make_uint2(g[j], r[2 * j + 1]) : make_uint2(r[2 * j], g[j]);
+  }
+  uint2 k[NH / 8];
+#pragma unroll
+  for (int j = 0; j < NH / 8; ++j) {  // head 8 j + 4 b2 + 2 b1 + b0, eight dims
+    const uint2 send = b2 ? u[2 * j] : u[2 * j + 1];
+    k[j] = make_uint2(__shfl_xor_sync(0xFFFFFFFFu, send.x, 4),
+                      __shfl_xor_sync(0xFFFFFFFFu, send.y, 4));
+  }
+  uint16_t* o = out + static_cast<int64_t>(h0 + (lane & 7)) * kLatent + d32 + (lane & 24);
+#pragma unroll
+  for (int j = 0; j < NH / 8; ++j) {
+    const uint4 w = b2 ? make_uint4(k[j].x, k[j].y, u[2 * j + 1].x, u[2 * j + 1].y)
+                       : make_uint4(u[2 * j].x, u[2 * j].y, k[j].x, k[j].y);
+    *reinterpret_cast<uint4*>(o + static_cast<int64_t>(8 * j) * kLatent) = w;
+  }
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -237,11 +249,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   // read while the previous kernel still selects the tokens), then its part of
   // the selected latents.
   const int64_t wrow0 = static_cast<int64_t>(b) * a.window;
-  const int w_part = (n_sw + S - 1) / S;
+  const int lg_s = 31 - __clz(S);
+  const int w_part = (n_sw + S - 1) >> lg_s;
   const int w_begin = min(n_sw, split * w_part);
   const int w_cnt = min(n_sw, w_begin + w_part) - w_begin;
   auto sel_range = [&](int n_sel, int& s_begin, int& s_cnt) {
-    const int h = (n_sel + S - 1) / S;
+    const int h = (n_sel + S - 1) >> lg_s;
     s_begin = min(n_sel, split * h);
     s_cnt = min(n_sel, s_begin + h) - s_begin;
   };
@@ -578,10 +591,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&misc->p_full);
     }
-    // the two halves' sums (the order is fixed)
+    // the two halves' sums (the order is fixed); with a split, (max, sum) to every CTA of
+    // the cluster, there by phase 1
     if (half == 1) misc->mx[0][0][h] = l_run;
     named_sync(kMathBar, 128);
     if (half == 0) l_run += misc->mx[0][0][h];
+    if (paired) {
+      cluster_wait();  // phase 0: every CTA's barriers are initialised
+      if (half == 0) {
+        const uint32_t mine = sbase + kMl + static_cast<uint32_t>(split * kHeads + h) * 8u;
+        for (int p = 0; p < S; ++p) {
+          st_cluster_f32x2(mapa_shared(mine, static_cast<uint32_t>(p)),
+                           ok && n_tiles > 0 ? m_run : -INFINITY, ok ? l_run : 0.f);
+        }
+      }
+    }
   }
 
   if (warp < kMmaWarp) {
@@ -603,170 +627,148 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const bool have_o = ok && n_tiles > 0;
     uint16_t* out = a.out + static_cast<int64_t>(b) * kHeads * kLatent;
-    auto load32 = [&](int m, int hp, float (&v)[32]) {  // heads 32 hp .. + 31
+    // v = heads 32 hp .. + 31 of slice m's dim in this lane, times their weights
+    auto load32 = [&](int m, int hp, float (&v)[32]) {
       if (have_o) {
         tmem_ld32(lq + 64 * m + 32 * hp, v);
       } else {
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = 0.f;
       }
+      const uint32_t f = smem_u32(misc->wgt) + 128u * hp;
+#pragma unroll
+      for (int i = 0; i < 32; i += 4) {
+        const float4 w4 = ld_shared_f4(f + 4u * i);
+        v[i] *= w4.x;
+        v[i + 1] *= w4.y;
+        v[i + 2] *= w4.z;
+        v[i + 3] *= w4.w;
+      }
     };
-    if (!paired) {
-      if (warp < 2) {
-        misc->inv_l[tid] = l_run > 0.f ? 1.f / l_run : 0.f;
-        if (a.lse) {
-          a.lse[static_cast<int64_t>(b) * kHeads + tid] =
-              l_run > 0.f ? (m_run + log2f(l_run)) * 0.69314718055994531f : -INFINITY;
+    if (paired) {
+      if (warp >= kLoadWarp0) cluster_wait();  // phase 0 (the math warps have waited)
+      // phase 1: every CTA's MMAs are done, so its slots may be written, and every
+      // CTA's (max, sum) is here
+      cluster_arrive();
+      cluster_wait();
+    }
+    // The weight of this CTA's O: 2^(m - M) / L with M = max_q m_q, L = sum_q 2^(m_q - M) l_q
+    // over the cluster's CTAs (a range without rows has l_q = 0).
+    if (warp < 2) {
+      float M = m_run, L = l_run;
+      if (paired) {
+        const float2* ml = reinterpret_cast<const float2*>(gbase + kMl) + tid;
+        float2 x[kMaxAttnSplits];
+        M = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < kMaxAttnSplits; ++q) {
+          x[q] = q < S ? ml[q * kHeads] : make_float2(-INFINITY, 0.f);
+        }
+#pragma unroll
+        for (int q = 0; q < kMaxAttnSplits; ++q) {
+          if (!(x[q].y <= 0.f)) M = fmaxf(M, x[q].x);  // (a NaN counts)
+        }
+        L = 0.f;
+#pragma unroll
+        for (int q = 0; q < kMaxAttnSplits; ++q) {
+          if (!(x[q].y <= 0.f)) L = fmaf(ex2_ftz(x[q].x - M), x[q].y, L);
         }
       }
-      named_sync(kEpiBar, kEpiThreads);
-      const uint32_t inv_l_s = smem_u32(misc->inv_l);
+      misc->wgt[tid] = L == 0.f || !have_o ? 0.f : ex2_ftz(m_run - M) / L;
+      if (a.lse && split == 0) {
+        a.lse[static_cast<int64_t>(b) * kHeads + tid] =
+            L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+      }
+    }
+    named_sync(kEpiBar, kEpiThreads);
+    if (!paired) {
 #pragma unroll 1
       for (int i = grp; i < 8; i += kEpiGroups) {
         float v[32];
         load32(i >> 1, i & 1, v);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float o[8];
-#pragma unroll
-          for (int e = 0; e < 8; e += 4) {
-            const float4 f = ld_shared_f4(inv_l_s + (32 * (i & 1) + 8 * c + e) * 4);
-            o[e] = v[8 * c + e] * f.x;
-            o[e + 1] = v[8 * c + e + 1] * f.y;
-            o[e + 2] = v[8 * c + e + 2] * f.z;
-            o[e + 3] = v[8 * c + e + 3] * f.w;
-          }
-          store_heads8(out, 32 * (i & 1) + 8 * c, 128 * (i >> 1) + et0, lane, o);
-        }
+        store_heads<32>(out, 32 * (i & 1), 128 * (i >> 1) + et0, lane, v);
       }
     } else {
       // CTA `split` finishes dims [split D, split D + D). Each CTA writes its part for
-      // each CTA straight into that one's receive area (its slots, free once its MMAs
-      // are done). A warp's 32 dims always go to one CTA.
-      const int D = kLatent / S, lg_d = 31 - __clz(D);
+      // each CTA straight into that one's receive area (its slots). A warp's 32 dims
+      // always go to one CTA.
+      const int D = kLatent >> lg_s, lg_d = 9 - lg_s;
       const uint32_t pay = static_cast<uint32_t>(xchg_bytes(S));
-      const uint32_t off_ml = static_cast<uint32_t>(xchg_ml(S));
       const uint32_t plane = static_cast<uint32_t>(D) * 16u;
-      const float m_own = have_o ? m_run : -INFINITY, l_own = have_o ? l_run : 0.f;
-      auto recv_slot = [&](int q) -> uint32_t {  // what CTA q sent, in this CTA
-        return sbase + kKV + static_cast<uint32_t>(q) * pay;
-      };
-      cluster_wait();    // phase 0: every CTA's barriers are initialised
-      cluster_arrive();  // phase 1: every CTA's MMAs are done, so its slots may be written
-      cluster_wait();
 #pragma unroll 1
       for (int i = grp; i < 8; i += kEpiGroups) {
         const int m = i >> 1, hp = i & 1;
         const int d = 128 * m + et0 + lane;
         const int p = d >> lg_d;
-        const uint32_t mine = recv_slot(split) + static_cast<uint32_t>(d - p * D) * 16u;
-        const uint32_t area = mapa_shared(mine, static_cast<uint32_t>(p));
+        const uint32_t mine = sbase + kKV + static_cast<uint32_t>(split) * pay +
+                              static_cast<uint32_t>(d - p * D) * 16u +
+                              static_cast<uint32_t>(4 * hp) * plane;
+        const uint32_t mine_lo = mine + static_cast<uint32_t>(8 - 2 * hp) * plane;
         float v[32];
         load32(m, hp, v);
+        uint4 hi[4], lo[2];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {  // 16 heads
-          uint32_t hi[8], lo[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            // the upper 24 bits, rounded half up (a carry into the exponent is right
-            // too; a NaN's bits take no carry)
-            uint32_t x[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float f = v[16 * c + 4 * e + k];
-              x[k] = f == f ? __float_as_uint(f) + 0x80u : 0x7FC00000u;
-            }
-            hi[2 * e] = prmt(x[0], x[1], 0x7632u);
-            hi[2 * e + 1] = prmt(x[2], x[3], 0x7632u);
-            lo[e] = prmt(prmt(x[0], x[1], 0x0051u), prmt(x[2], x[3], 0x0051u), 0x5410u);
-          }
-          const uint32_t u = static_cast<uint32_t>(4 * hp + 2 * c);
-          const uint4 h0 = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          const uint4 h1 = make_uint4(hi[4], hi[5], hi[6], hi[7]);
-          const uint4 l0 = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          if (p == split) {  // its own part, by plain stores
-            st_shared_v4(mine + u * plane, h0);
-            st_shared_v4(mine + (u + 1u) * plane, h1);
-            st_shared_v4(mine + (8u + (u >> 1)) * plane, l0);
-          } else {
-            st_cluster_u4(area + u * plane, h0);
-            st_cluster_u4(area + (u + 1u) * plane, h1);
-            st_cluster_u4(area + (8u + (u >> 1)) * plane, l0);
-          }
+        for (int c = 0; c < 4; ++c) {  // 8 heads: the upper 16 bits ...
+          const float* x = v + 8 * c;
+          auto up = [&](int k) {
+            return prmt(__float_as_uint(x[2 * k]), __float_as_uint(x[2 * k + 1]), 0x7632u);
+          };
+          hi[c] = make_uint4(up(0), up(1), up(2), up(3));
         }
-      }
-      if (warp < 2) {
-        for (int p = 0; p < S; ++p) {
-          st_cluster_f32x2(mapa_shared(recv_slot(split) + off_ml + 8 * tid, static_cast<uint32_t>(p)),
-                           m_own, l_own);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {  // 16 heads: ... and the next 8
+          const float* x = v + 16 * c;
+          auto next = [&](int k) {
+            return prmt(prmt(__float_as_uint(x[4 * k]), __float_as_uint(x[4 * k + 1]), 0x0051u),
+                        prmt(__float_as_uint(x[4 * k + 2]), __float_as_uint(x[4 * k + 3]), 0x0051u),
+                        0x5410u);
+          };
+          lo[c] = make_uint4(next(0), next(1), next(2), next(3));
+        }
+        if (p == split) {  // its own part, by plain stores
+#pragma unroll
+          for (int c = 0; c < 4; ++c) st_shared_v4(mine + c * plane, hi[c]);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) st_shared_v4(mine_lo + c * plane, lo[c]);
+        } else {
+          const uint32_t there = mapa_shared(mine, static_cast<uint32_t>(p));
+          const uint32_t there_lo = there + (mine_lo - mine);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) st_cluster_u4(there + c * plane, hi[c]);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) st_cluster_u4(there_lo + c * plane, lo[c]);
         }
       }
       cluster_arrive();  // phase 2: everything is written (release) ...
       cluster_wait();    // ... and visible here (acquire)
-      // out = sum_q w_q O_q with w_q = 2^(m_q - M) / L, M = max_q m_q,
-      // L = sum_q 2^(m_q - M) l_q (a range without rows has l_q = 0). Eight
-      // lanes a head, one for each CTA of the cluster.
-      float* wgt = reinterpret_cast<float*>(gbase + kWgt);  // [S][64]
-      const int q = lane & 7;
+      // The output: the sum of the parts, (16 heads, 32 dims) pairs in turn over the warps.
 #pragma unroll 1
-      for (int h = 4 * warp + (lane >> 3); h < kHeads; h += kEpiThreads / 8) {
-        float2 x = make_float2(-INFINITY, 0.f);
-        if (q < S) {
-          x = reinterpret_cast<const float2*>(gbase + (recv_slot(q) - sbase) + off_ml)[h];
-        }
-        const bool some = !(x.y <= 0.f);  // (a NaN counts)
-        float M = some ? x.x : -INFINITY;
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-        const float e = some ? exp2f(x.x - M) : 0.f;
-        float L = e * x.y;
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, o);
-        if (q < S) wgt[q * kHeads + h] = L == 0.f ? 0.f : e / L;
-        if (a.lse && split == 0 && q == 0) {
-          a.lse[static_cast<int64_t>(b) * kHeads + h] =
-              L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
-        }
-      }
-      named_sync(kEpiBar, kEpiThreads);
-      const uint32_t wgt_s = sbase + kWgt;
-      // (16 heads, 32 dims) pairs, in turn over the warps
-#pragma unroll 1
-      for (int i = warp; i < 4 * (D / 32); i += kEpiThreads / 32) {
+      for (int i = warp; i < D >> 3; i += kEpiThreads / 32) {
         const uint32_t g = static_cast<uint32_t>(i & 3);
         const int d32 = 32 * (i >> 2);
         float v[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[e] = 0.f;
-        uint32_t src = sbase + kKV + static_cast<uint32_t>(d32 + lane) * 16u;
+        uint32_t src = sbase + kKV + static_cast<uint32_t>(d32 + lane) * 16u + 2u * g * plane;
+        const uint32_t to_lo = (8u - g) * plane;
 #pragma unroll 2
         for (int r = 0; r < S; ++r, src += pay) {
-          const uint4 x0 = ld_shared_v4(src + 2u * g * plane);
-          const uint4 x1 = ld_shared_v4(src + (2u * g + 1u) * plane);
-          const uint4 y = ld_shared_v4(src + (8u + g) * plane);
+          const uint4 x0 = ld_shared_v4(src);
+          const uint4 x1 = ld_shared_v4(src + plane);
+          const uint4 y = ld_shared_v4(src + to_lo);
           const uint32_t hi[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
           const uint32_t lo[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float4 w4 =
-                ld_shared_f4(wgt_s + (static_cast<uint32_t>(r) * kHeads + 16u * g + 4u * e) * 4u);
-            // bytes from the top: the 16-bit part, the 8-bit part, 0
-            const uint32_t b01 = hi[2 * e], b23 = hi[2 * e + 1], l4 = lo[e];
-            v[4 * e] = fmaf(w4.x, __uint_as_float(prmt(b01, l4, 0x1040u) & 0xFFFFFF00u), v[4 * e]);
-            v[4 * e + 1] =
-                fmaf(w4.y, __uint_as_float(prmt(b01, l4, 0x3250u) & 0xFFFFFF00u), v[4 * e + 1]);
-            v[4 * e + 2] =
-                fmaf(w4.z, __uint_as_float(prmt(b23, l4, 0x1060u) & 0xFFFFFF00u), v[4 * e + 2]);
-            v[4 * e + 3] =
-                fmaf(w4.w, __uint_as_float(prmt(b23, l4, 0x3270u) & 0xFFFFFF00u), v[4 * e + 3]);
+            // bytes from the top: the 16-bit part, the 8-bit part twice (the middle of
+            // what was cut off, to within 2^-17)
+            v[4 * e] += __uint_as_float(prmt(hi[2 * e], lo[e], 0x1044u));
+            v[4 * e + 1] += __uint_as_float(prmt(hi[2 * e], lo[e], 0x3255u));
+            v[4 * e + 2] += __uint_as_float(prmt(hi[2 * e + 1], lo[e], 0x1066u));
+            v[4 * e + 3] += __uint_as_float(prmt(hi[2 * e + 1], lo[e], 0x3277u));
           }
         }
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float o[8] = {v[8 * c],     v[8 * c + 1], v[8 * c + 2], v[8 * c + 3],
-                              v[8 * c + 4], v[8 * c + 5], v[8 * c + 6], v[8 * c + 7]};
-          store_heads8(out, 16 * static_cast<int>(g) + 8 * c, split * D + d32, lane, o);
-        }
+        store_heads<16>(out, 16 * static_cast<int>(g), split * D + d32, lane, v);
       }
     }
   }
