@@ -150,49 +150,25 @@ __device__ __noinline__ void report(DeviceStatus* st, uint32_t detail) {
   record_status(st, DSA_ERR_DEVICE_CHECK, SITE_ATTN, detail);
 }
 
-// out[h0 + i][d] = v[i] for NH heads, lane l holding dim d = d32 + l of a
-// 32-aligned range: three exchanges with lanes 1, 2 and 4 away leave each lane
-// 8 consecutive dims of one head in eight, so a warp writes 64 contiguous bytes of each
-// of eight heads by one 16-byte store a lane (2-byte stores, one head at a time,
-// take eight times as many).
+// bf16(v[i]) to row h0 + i of a shared-memory image of the output (`row` bytes a head), lane
+// l at dim d (2 bytes): a warp's lanes hold neighbouring dims, so a store touches
+// each bank once. The image then leaves by coalesced 16-byte stores. (From the
+// registers, 64-byte pieces of eight heads by exchanged 16-byte stores took 2300
+// clocks for every 32 heads x 384 dims; this takes 700. Bulk copies, one a head, took
+// a microsecond to read the image.)
 template <int NH>
-__device__ __forceinline__ void store_heads(uint16_t* out, int h0, int d32, int lane,
+__device__ __forceinline__ void stage_heads(uint32_t image, uint32_t row, int h0, int d,
                                             const float (&v)[NH]) {
-  const bool b0 = lane & 1, b1 = lane & 2, b2 = lane & 4;
-  uint32_t r[NH / 2];
+  const uint32_t at = image + static_cast<uint32_t>(h0) * row + 2u * static_cast<uint32_t>(d);
 #pragma unroll
-  for (int j = 0; j < NH / 2; ++j) {  // head 2 j + b0, two dims
-    const __nv_bfloat162 x = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-    r[j] = *reinterpret_cast<const uint32_t*>(&x);
-  }
-  uint32_t g[NH / 2];
-#pragma unroll
-  for (int j = 0; j < NH / 2; ++j) g[j] = __shfl_xor_sync(0xFFFFFFFFu, r[j], 1);
-  const uint32_t sel = b0 ? 0x3276u : 0x5410u;
-#pragma unroll
-  for (int j = 0; j < NH / 2; ++j) r[j] = prmt(r[j], g[j], sel);
-#pragma unroll
-  for (int j = 0; j < NH / 4; ++j) {  // head 4 j + 2 b1 + b0, four dims
-    g[j] = __shfl_xor_sync(0xFFFFFFFFu, b1 ? r[2 * j] : r[2 * j + 1], 2);
-  }
-  uint2 u[NH / 4];
-#pragma unroll
-  for (int j = 0; j < NH / 4; ++j) {
-    u[j] = b1 ? make_uint2(g[j], r[2 * j + 1]) : make_uint2(r[2 * j], g[j]);
-  }
-  uint2 k[NH / 8];
-#pragma unroll
-  for (int j = 0; j < NH / 8; ++j) {  // head 8 j + 4 b2 + 2 b1 + b0, eight dims
-    const uint2 send = b2 ? u[2 * j] : u[2 * j + 1];
-    k[j] = make_uint2(__shfl_xor_sync(0xFFFFFFFFu, send.x, 4),
-                      __shfl_xor_sync(0xFFFFFFFFu, send.y, 4));
-  }
-  uint16_t* o = out + static_cast<int64_t>(h0 + (lane & 7)) * kLatent + d32 + (lane & 24);
-#pragma unroll
-  for (int j = 0; j < NH / 8; ++j) {
-    const uint4 w = b2 ? make_uint4(k[j].x, k[j].y, u[2 * j + 1].x, u[2 * j + 1].y)
-                       : make_uint4(u[2 * j].x, u[2 * j].y, k[j].x, k[j].y);
-    *reinterpret_cast<uint4*>(o + static_cast<int64_t>(8 * j) * kLatent) = w;
+  for (int j = 0; j < NH; j += 2) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(v[j], v[j + 1]);
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(&x);
+    asm volatile(
+        "{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n st.shared.b16 [%0], a;\n"
+        " st.shared.b16 [%1], b;\n}\n" ::"r"(at + j * row),
+        "r"(at + (j + 1) * row), "r"(w)
+        : "memory");
   }
 }
 
@@ -675,18 +651,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       misc->wgt[tid] = L == 0.f || !have_o ? 0.f : ex2_ftz(m_run - M) / L;
-      if (a.lse && split == 0) {
-        a.lse[static_cast<int64_t>(b) * kHeads + tid] =
-            L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
-      }
+      m_run = M;  // for the log-sum-exp at the end
+      l_run = L;
     }
     named_sync(kEpiBar, kEpiThreads);
+    const uint32_t image = sbase + kQ;  // Q is no longer read
     if (!paired) {
 #pragma unroll 1
       for (int i = grp; i < 8; i += kEpiGroups) {
         float v[32];
         load32(i >> 1, i & 1, v);
-        store_heads<32>(out, 32 * (i & 1), 128 * (i >> 1) + et0, lane, v);
+        stage_heads<32>(image, kLatent * 2, 32 * (i & 1), 128 * (i >> 1) + et0 + lane, v);
       }
     } else {
       // CTA `split` finishes dims [split D, split D + D). Each CTA writes its part for
@@ -768,8 +743,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             v[4 * e + 3] += __uint_as_float(prmt(hi[2 * e + 1], lo[e], 0x3277u));
           }
         }
-        store_heads<16>(out, 16 * static_cast<int>(g), split * D + d32, lane, v);
+        stage_heads<16>(image, static_cast<uint32_t>(2 * D), 16 * static_cast<int>(g), d32 + lane,
+                        v);
       }
+    }
+    named_sync(kEpiBar, kEpiThreads);
+    {
+      // 16-byte unit k of the image is unit k % (D / 8) of head k / (D / 8)
+      const int lg_u = 6 - lg_s;
+      uint16_t* dst = out + split * (kLatent >> lg_s);
+      const int n = kHeads << lg_u;
+#pragma unroll 4
+      for (int k = tid; k < n; k += kEpiThreads) {
+        const uint4 x = ld_shared_v4(image + 16u * static_cast<uint32_t>(k));
+        *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(k >> lg_u) * kLatent +
+                                  8 * (k & ((1 << lg_u) - 1))) = x;
+      }
+    }
+    if (warp < 2 && a.lse && split == 0) {
+      a.lse[static_cast<int64_t>(b) * kHeads + tid] =
+          l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f;
     }
   }
 
