@@ -1110,6 +1110,7 @@ dsa_status_t dsa_norm_rope(int n, const int32_t* n_valid, const int32_t* positio
     sg.heads = h.heads;
     sg.dim = h.dim;
     while ((8 << sg.lanes_log2) < h.dim && sg.lanes_log2 < 5) ++sg.lanes_log2;
+    sg.unit_begin = static_cast<int>(units);
     units += (int64_t{h.heads} + (32 >> sg.lanes_log2) - 1) / (32 >> sg.lanes_log2);
     if (units > (1 << 24)) return DSA_ERR_UNSUPPORTED;
     sg.unit_end = static_cast<int>(units);
@@ -1121,6 +1122,7 @@ dsa_status_t dsa_norm_rope(int n, const int32_t* n_valid, const int32_t* positio
     max_dim = std::max(max_dim, h.dim);
   }
   if (n == 0 || units == 0) return DSA_OK;
+  if (int64_t{n} * units > (int64_t{1} << 40)) return DSA_ERR_UNSUPPORTED;
   a.n = n;
   a.n_valid = n_valid;
   a.positions = positions;

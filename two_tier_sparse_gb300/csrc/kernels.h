@@ -305,7 +305,7 @@ struct NormRopeSeg {
   const float* weight;  // [dim] or null
   int heads, dim;
   int lanes_log2;       // lanes of a warp that hold one head
-  int unit_end;         // units (warps' worth of heads) up to and with this group
+  int unit_begin, unit_end;  // the group's units (warps' worth of heads) of a token
   int norm, rope, rope_start;
   float eps, inv_dim;
 };
@@ -314,9 +314,11 @@ struct NormRopeArgs {
   const int32_t* n_valid;  // device count of tokens, or null
   const int32_t* positions;
   const double* inv_freq;  // [pairs]
+  uint64_t inv_2pi;        // 2^66 / (2 pi) (set by the launch)
   int pairs, interleaved;
   float rope_scale;
-  int units, units_per_cta;  // warps' worth of heads of a token, and of a CTA (set by the launch)
+  int units;       // warps' worth of heads of a token
+  int warp_bytes;  // shared memory of a warp (set by the launch)
   NormRopeSeg seg[DSA_MAX_HEAD_GROUPS];
 };
 cudaError_t launch_norm_rope(const NormRopeArgs& a, int dtype, int max_dim, cudaStream_t s);
