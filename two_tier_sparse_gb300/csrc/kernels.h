@@ -323,9 +323,16 @@ struct NormRopeArgs {
 };
 cudaError_t launch_norm_rope(const NormRopeArgs& a, int dtype, int max_dim, cudaStream_t s);
 
+// A divisor as a multiplication and a shift (csrc/plan.cu).
+struct Divisor {
+  uint32_t mul;
+  int shift;
+};
+
 // The plan of a step (dsa_plan_step).
 struct PlanArgs {
   int B, ratio, window;
+  Divisor by_ratio, by_rows, by_window;  // (set by the launch)
   const int32_t* n_tokens;
   const int32_t* n_new;
   int32_t* table;

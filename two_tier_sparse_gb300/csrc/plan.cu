@@ -12,7 +12,9 @@
 // ones together are at most the pool, the ring's size. What may be updated in
 // place (lengths, the ring's counters) is written by the last CTA to finish,
 // when all have read it. The work is a few integer operations a token and four
-// words written, so a small step costs its launch and two dependent reads.
+// words written, so a small step costs its launch and two dependent reads: the
+// lengths, then the table or the ring. Divisions are by constants of the call
+// (page_rows, ratio, window), as a multiplication and a shift.
 #include <algorithm>
 
 #include "kernels.h"
@@ -24,42 +26,55 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kPer = 4;  // consecutive tokens a thread takes: one 16-byte store an array
 
-struct Sums {
-  int64_t tok, pop, push;
-};
-__device__ __forceinline__ Sums operator+(const Sums& a, const Sums& b) {
-  return Sums{a.tok + b.tok, a.pop + b.pop, a.push + b.push};
-}
-__device__ __forceinline__ Sums shfl_up(const Sums& v, int o) {
-  return Sums{__shfl_up_sync(0xFFFFFFFFu, v.tok, o), __shfl_up_sync(0xFFFFFFFFu, v.pop, o),
-              __shfl_up_sync(0xFFFFFFFFu, v.push, o)};
+// n / d for 0 <= n < 2^31: (n + floor(n mul / 2^32)) / 2^shift with shift = ceil(log2 d) and
+// mul = floor(2^32 (2^shift - d) / d) + 1 (Granlund and Montgomery, "Division by invariant
+// integers using multiplication", 1994).
+__device__ __forceinline__ int div_by(int n, const Divisor& d) {
+  return static_cast<int>((__umulhi(static_cast<uint32_t>(n), d.mul) + static_cast<uint32_t>(n)) >>
+                          d.shift);
 }
 
-// What one request adds: new tokens, pages popped and pushed. `bad`: lengths
-// that no request can have.
-__device__ __forceinline__ Sums request(const PlanArgs& a, int b, bool& bad) {
-  const int n = a.n_tokens[b], add = a.n_new[b];
-  const int R = a.page_rows;
+// Sums over requests, each held at its own cap (one more than what is possible), so that
+// 32 bits do.
+struct Sums {
+  uint32_t tok, pop, push;
+};
+__device__ __forceinline__ Sums add(const Sums& a, const Sums& b, const Sums& cap) {
+  return Sums{min(a.tok + b.tok, cap.tok), min(a.pop + b.pop, cap.pop), min(a.push + b.push, cap.push)};
+}
+
+// What one request adds: new tokens, pages popped and pushed; `have` pages now. `bad`:
+// lengths that no request can have.
+__device__ __forceinline__ Sums request(const PlanArgs& a, int n, int more, int& have, bool& bad) {
+  const Sums none{0, 0, 0};
+  have = 0;
   if (n < 0) {
     bad = true;
-    return Sums{0, 0, 0};
+    return none;
   }
-  const int have = (n / a.ratio + R - 1) / R;
+  const int lat = div_by(n, a.by_ratio);
+  have = div_by(lat, a.by_rows);
+  have += have * a.page_rows < lat;
   if (have > a.pages_per_seq) {
     bad = true;
-    return Sums{0, 0, 0};
+    return none;
   }
-  if (add < 0) return Sums{0, 0, have};  // the request ends
-  const int64_t after = int64_t{n} + add;
-  const int64_t need = (after / a.ratio + R - 1) / R;
-  if (after > 0x7FFFFFFF || need > a.pages_per_seq) {
+  if (more < 0) return Sums{0, 0, static_cast<uint32_t>(have)};  // the request ends
+  if (more > 0x7FFFFFFF - n) {
     bad = true;
-    return Sums{0, 0, 0};
+    return none;
   }
-  return Sums{add, need - have, 0};
+  const int lat1 = div_by(n + more, a.by_ratio);
+  int need = div_by(lat1, a.by_rows);
+  need += need * a.page_rows < lat1;
+  if (need > a.pages_per_seq) {
+    bad = true;
+    return none;
+  }
+  return Sums{static_cast<uint32_t>(more), static_cast<uint32_t>(need - have), 0};
 }
 
-// The last b with first[b] <= i, first[] ascending with first[0] = 0.
+// The last b with first[b] <= i, first[] ascending with first[0] = 0 and first[B] > i.
 __device__ __forceinline__ int find(const int* first, int B, int i) {
   int lo = 0, hi = B;  // first[lo] <= i < first[hi]
   while (hi - lo > 1) {
@@ -73,50 +88,68 @@ __device__ __forceinline__ int find(const int* first, int B, int i) {
   return lo;
 }
 
-__global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs a) {
+__global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ PlanArgs a) {
   extern __shared__ int sm[];
   int* cu = sm;                    // [B + 1] new tokens before request b
   int* pop = cu + a.B + 1;         // [B + 1] pages popped
   int* push = pop + a.B + 1;       // [B + 1] pages pushed
+  int* len = push + a.B + 1;       // [B] lengths before the step
+  int* held = len + a.B;           // [B] pages before the step
   __shared__ Sums warp_sum[kThreads / 32];
-  __shared__ int any_bad;
-  griddep_wait();
+  __shared__ int any_bad, last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int R = a.page_rows;
-  const int64_t head = a.ring_state[0], tail = a.ring_state[1];
+  const Sums cap{static_cast<uint32_t>(a.max_new) + 1u, static_cast<uint32_t>(a.n_pages) + 1u,
+                 static_cast<uint32_t>(a.n_pages) + 1u};
   if (tid == 0) any_bad = 0;
-  __syncthreads();
+  griddep_wait();
+  const int64_t head = a.ring_state[0], tail = a.ring_state[1];
 
   // Prefix sums: a thread takes `per` consecutive requests.
   const int per = (a.B + kThreads - 1) / kThreads;
   const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
   bool bad = false;
   Sums own{0, 0, 0};
-  for (int b = b0; b < b1; ++b) own = own + request(a, b, bad);
+  for (int b = b0; b < b1; ++b) {
+    const int n = a.n_tokens[b], more = a.n_new[b];
+    int have;
+    const Sums r = request(a, n, more, have, bad);
+    len[b] = n;
+    held[b] = have;
+    cu[b] = static_cast<int>(own.tok);  // (within the thread's requests, for now)
+    pop[b] = static_cast<int>(own.pop);
+    push[b] = static_cast<int>(own.push);
+    own = add(own, r, cap);
+  }
   Sums incl = own;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const Sums t = shfl_up(incl, o);
-    if (lane >= o) incl = incl + t;
+    const Sums t{__shfl_up_sync(0xFFFFFFFFu, incl.tok, o), __shfl_up_sync(0xFFFFFFFFu, incl.pop, o),
+                 __shfl_up_sync(0xFFFFFFFFu, incl.push, o)};
+    if (lane >= o) incl = add(incl, t, cap);
   }
   if (lane == 31) warp_sum[warp] = incl;
+  Sums before{__shfl_up_sync(0xFFFFFFFFu, incl.tok, 1), __shfl_up_sync(0xFFFFFFFFu, incl.pop, 1),
+              __shfl_up_sync(0xFFFFFFFFu, incl.push, 1)};
+  if (lane == 0) before = Sums{0, 0, 0};
+  __syncthreads();  // any_bad is cleared, the warps' sums are written
   if (bad) any_bad = 1;
-  __syncthreads();
-  Sums before{incl.tok - own.tok, incl.pop - own.pop, incl.push - own.push}, total{0, 0, 0};
+  Sums total{0, 0, 0};
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before = before + warp_sum[w];
-    total = total + warp_sum[w];
+    if (w == warp) before = add(before, total, cap);
+    total = add(total, warp_sum[w], cap);
   }
+  __syncthreads();  // any_bad is known
   // All or nothing: the same decision in every CTA.
-  const bool ok = !any_bad && total.tok <= a.max_new && head >= 0 && tail >= head &&
-                  total.pop <= tail - head && tail - head + total.push <= a.n_pages;
-  Sums at = before;
+  const int64_t free_pages = tail - head;
+  const bool ok = !any_bad && total.tok <= static_cast<uint32_t>(a.max_new) && head >= 0 &&
+                  free_pages >= 0 && total.pop <= free_pages &&
+                  free_pages + total.push <= a.n_pages;
   for (int b = b0; b < b1; ++b) {
-    cu[b] = ok ? static_cast<int>(at.tok) : 0;
-    pop[b] = ok ? static_cast<int>(at.pop) : 0;
-    push[b] = ok ? static_cast<int>(at.push) : 0;
-    at = at + request(a, b, bad);
+    cu[b] = ok ? cu[b] + static_cast<int>(before.tok) : 0;
+    pop[b] = ok ? pop[b] + static_cast<int>(before.pop) : 0;
+    push[b] = ok ? push[b] + static_cast<int>(before.push) : 0;
   }
   if (tid == 0) {
     cu[a.B] = ok ? static_cast<int>(total.tok) : 0;
@@ -134,50 +167,54 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs a) {
     return static_cast<int>(i >= a.n_pages ? i - a.n_pages : i);
   };
 
-  // The table's new entries, and the pages of ended requests back to the ring.
-  for (int k = gtid; k < n_pop; k += gstep) {
+  // The table's new entries, and the pages of ended requests back to the ring: from the
+  // grid's last thread down, so that in a small step they fall to other warps than the
+  // tokens.
+  for (int k = gstep - 1 - gtid; k < n_pop; k += gstep) {
     const int b = find(pop, a.B, k);
-    const int have = (a.n_tokens[b] / a.ratio + R - 1) / R;
-    a.table[static_cast<int64_t>(b) * a.pages_per_seq + have + (k - pop[b])] =
+    a.table[static_cast<int64_t>(b) * a.pages_per_seq + held[b] + (k - pop[b])] =
         a.ring[ring_at(head_m, k)];
   }
-  for (int k = gtid; k < n_push; k += gstep) {
+  for (int k = gstep - 1 - gtid; k < n_push; k += gstep) {
     const int b = find(push, a.B, k);
     a.ring[ring_at(tail_m, k)] = a.table[static_cast<int64_t>(b) * a.pages_per_seq + (k - push[b])];
   }
 
   // Tokens: kPer consecutive ones a thread; rows past the last token are empty.
   for (int i0 = kPer * gtid; i0 < a.max_new; i0 += kPer * gstep) {
-    int seq[kPer], pos[kPer], lslot[kPer], wslot[kPer];
+    int seq[kPer], pos[kPer], lslot[kPer], wslot[kPer], page[kPer];
     int b = i0 < n_tok ? find(cu, a.B, i0) : 0;
-    int nb = -1, n = 0, have = 0, after = 0;  // of request nb
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       const int i = i0 + k;
       seq[k] = lslot[k] = wslot[k] = -1;
       pos[k] = 0;
+      page[k] = 0;
       if (i < n_tok) {
         while (i >= cu[b + 1]) ++b;
-        if (b != nb) {
-          nb = b;
-          n = a.n_tokens[b];
-          have = (n / a.ratio + R - 1) / R;
-          after = n + (cu[b + 1] - cu[b]);
-        }
-        const int p = n + (i - cu[b]);
+        const int n = len[b], p = n + (i - cu[b]), after = n + (cu[b + 1] - cu[b]);
         seq[k] = b;
         pos[k] = p;
-        if (p >= after - a.window) wslot[k] = b * a.window + p % a.window;
-        const int j = (p + 1) / a.ratio - 1;
-        if ((j + 1) * a.ratio == p + 1) {  // the token completes latent j
-          const int pg = j / R;
-          const int page = pg < have ? a.table[static_cast<int64_t>(b) * a.pages_per_seq + pg]
-                                     : a.ring[ring_at(head_m, pop[b] + pg - have)];
-          if (page >= 0 && page < a.n_pages) {
-            lslot[k] = page * R + (j - pg * R);
-          } else {
-            record_status(a.status, DSA_ERR_DEVICE_CHECK, SITE_PLAN, static_cast<uint32_t>(b));
-          }
+        if (p >= after - a.window) {
+          wslot[k] = b * a.window + (p - div_by(p, a.by_window) * a.window);
+        }
+        const int done = div_by(p + 1, a.by_ratio);
+        if (done * a.ratio == p + 1) {  // the token completes latent done - 1
+          const int j = done - 1, pg = div_by(j, a.by_rows), have = held[b];
+          lslot[k] = j - pg * R;
+          page[k] = pg < have ? a.table[static_cast<int64_t>(b) * a.pages_per_seq + pg]
+                              : a.ring[ring_at(head_m, pop[b] + pg - have)];
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      if (lslot[k] >= 0) {
+        if (page[k] >= 0 && page[k] < a.n_pages) {
+          lslot[k] += page[k] * R;
+        } else {
+          lslot[k] = -1;
+          record_status(a.status, DSA_ERR_DEVICE_CHECK, SITE_PLAN, static_cast<uint32_t>(seq[k]));
         }
       }
     }
@@ -204,29 +241,26 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs a) {
   // Per request. The lengths and the ring's counters may be updated in place:
   // the last CTA writes them, when every CTA has read what it needs.
   auto after_of = [&](int b) -> int {
-    const int n = a.n_tokens[b];
-    if (!ok) return n;
-    return a.n_new[b] < 0 ? 0 : n + (cu[b + 1] - cu[b]);
+    if (!ok) return len[b];
+    return push[b + 1] > push[b] || a.n_new[b] < 0 ? 0 : len[b] + (cu[b + 1] - cu[b]);
   };
   for (int b = gtid; b <= a.B; b += gstep) {
     a.cu_new[b] = cu[b];
     if (b < a.B) {
       const int n = max(after_of(b), 0);
-      a.n_latents[b] = n / a.ratio;
+      a.n_latents[b] = div_by(n, a.by_ratio);
       a.swa_len[b] = min(n, a.window);
     }
   }
-  __shared__ int last;
-  __syncthreads();
-  if (tid == 0) {
-    last = 1;
-    if (gridDim.x > 1) {
+  if (gridDim.x > 1) {
+    __syncthreads();
+    if (tid == 0) {
       last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
       if (last) *a.ticket = 0u;
     }
+    __syncthreads();
+    if (!last) return;
   }
-  __syncthreads();
-  if (!last) return;
   for (int b = tid; b < a.B; b += kThreads) a.n_tokens_out[b] = after_of(b);
   if (tid == 0) {
     a.ring_state_out[0] = ok ? head + total.pop : head;
@@ -234,13 +268,25 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs a) {
   }
 }
 
+Divisor divisor(int d) {
+  Divisor r;
+  r.shift = 0;
+  while ((int64_t{1} << r.shift) < d) ++r.shift;
+  r.mul = static_cast<uint32_t>(((uint64_t{1} << 32) * ((uint64_t{1} << r.shift) - d)) / d + 1);
+  return r;
+}
+
 }  // namespace
 
-cudaError_t launch_plan(const PlanArgs& a, cudaStream_t s) {
-  const int smem = 3 * (a.B + 1) * 4;
+cudaError_t launch_plan(const PlanArgs& args, cudaStream_t s) {
+  PlanArgs a = args;
+  a.by_ratio = divisor(a.ratio);
+  a.by_rows = divisor(a.page_rows);
+  a.by_window = divisor(a.window);
+  const int smem = (5 * a.B + 3) * 4;
   static std::atomic<int> smem_set[64]{};
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(plan_kernel),
-                              3 * (DSA_PLAN_MAX_REQUESTS + 1) * 4, smem_set);
+                              (5 * DSA_PLAN_MAX_REQUESTS + 3) * 4, smem_set);
   if (e != cudaSuccess) return e;
   // A CTA for every 2048 tokens (each thread one group of four), at most one an SM.
   const int64_t want = (static_cast<int64_t>(a.max_new) + kPer * kThreads - 1) / (kPer * kThreads);
