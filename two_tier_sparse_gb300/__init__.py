@@ -160,15 +160,18 @@ def _check(code: int, where: str) -> None:
         raise DsaError(code, where)
 
 
+# Pointers and streams travel as plain integers (every argument is declared void*):
+# building ctypes objects for them cost more than the call itself.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch.cuda.current_device
+
+
 def _p(t: Optional[torch.Tensor]):
-    if t is None:
-        return None
-    return ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    return _raw_stream(_current_device()) if stream is None else stream.cuda_stream
 
 
 def config(k_blocks=2048, k_tokens=512, window=128, ratio=1, sm_scale=0.0, kv_fmt=KV_BF16,
@@ -334,10 +337,9 @@ def _launch_stream(t: torch.Tensor, stream):
     """The raw stream to launch on: the given one, or the current stream of t's
     device, which has to be the current device (the library launches there)."""
     dev = t.get_device()
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"tensors on device {dev}, but the current device is "
-                         f"{torch.cuda.current_device()}")
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
+    if dev != _current_device():
+        raise ValueError(f"tensors on device {dev}, but the current device is {_current_device()}")
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
 def _i32(name, t, shape=None, optional=False):
@@ -519,16 +521,18 @@ def _rows_call(cfg, rows, slots, cache, n_valid):
     row = _KV_ROW.get(cfg.kv_fmt)
     if row is None:
         raise DsaError(1, "kv_fmt")
-    if rows.dtype not in (torch.bfloat16, torch.int16) or rows.dim() != 2 or \
-            rows.shape[1] != 512 or rows.stride(1) != 1:
+    shape, stride = rows.shape, rows.stride()
+    if _DT.get(rows.dtype) != 0 or len(shape) != 2 or shape[1] != 512 or stride[1] != 1:
         raise ValueError("rows: bf16 (or its bits in int16) [n, 512] with contiguous elements")
-    n = rows.shape[0]
-    _i32("slots", slots, (n,))
-    _i32("n_valid", n_valid, (1,), optional=True)
-    size = cache.numel() * cache.element_size()
-    if not cache.is_contiguous() or cache.shape[-1] * cache.element_size() != row:
+    n = shape[0]
+    if slots.dtype is not torch.int32 or slots.shape != shape[:1] or not slots.is_contiguous():
+        _i32("slots", slots, (n,))
+    if n_valid is not None:
+        _i32("n_valid", n_valid, (1,))
+    width = cache.element_size()
+    if not cache.is_contiguous() or cache.shape[-1] * width != row:
         raise ValueError(f"cache: contiguous rows of {row} bytes")
-    return n, rows.stride(0), size // row
+    return n, stride[0], cache.numel() * width // row
 
 
 def kv_write(cfg, rows, slots, cache, ws, n_valid=None, stream=None):
