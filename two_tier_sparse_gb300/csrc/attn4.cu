@@ -5,7 +5,7 @@
 //   S   = Q . KV^T    (.ws, M = 64 heads, N = 64 rows, K = 512: rows 0..31 in lanes 0..63,
 //                      rows 32..63 in lanes 64..127, 32 columns)
 //   O^T += KV^T . P^T (four M = 128 slices of the 512 latent dims, N = 64 heads,
-//                      K = 64 rows; the KV tile is read as an MN-major operand)
+//                      K = the tile's rows; the KV tile is read as an MN-major operand)
 //
 // A row is 272 bytes, so a tile's rows fit in registers on their way: eight
 // loader warps read a tile's codes (16 bytes a lane: 32 elements, one scale)
@@ -38,11 +38,10 @@ namespace dsa {
 
 namespace {
 
-constexpr int kRows = 64;                          // rows of a tile
-constexpr int kSlots = 2;
+constexpr int kN = 64;                             // rows of a QK^T MMA
+constexpr int kHalf = kN / 2;                      // scores of a math thread
 constexpr int kLoadWarp0 = 4;
 constexpr int kLoadWarps = 8;
-constexpr int kWarpRows = kRows / kLoadWarps;      // 8 rows of a tile for each loader warp
 constexpr int kMmaWarp = kLoadWarp0 + kLoadWarps;  // 12: QK^T issuer (and TMEM owner)
 constexpr int kPvWarp = kMmaWarp + 1;              // 13: PV issuer
 constexpr int kThreads = 32 * (kPvWarp + 1);       // 448
@@ -51,21 +50,35 @@ constexpr int kEpiBar = 2;                         // of the epilogue (math and 
 constexpr int kEpiThreads = 32 * kMmaWarp;         // 384
 constexpr int kEpiGroups = kEpiThreads / 128;      // 3 groups of four warps (TMEM lane quarters)
 
-// Shared memory, offsets from a 1024-aligned base.
-constexpr int kAtomBytes = kRows * 128;            // 64 dims of a tile's rows
-constexpr int kSlotBytes = 8 * kAtomBytes;
+// Tiles of ROWS rows and the shared memory they make, offsets from a 1024-aligned base.
+// Two slots of 64 rows, or three of 48: with three, loads, softmax and MMAs of more tiles
+// overlap, but a QK^T step still takes the time of 64 rows (it reads 16 rows past each
+// atom, into what follows, and their scores are not used). A cluster of eight CTAs has
+// at most 80 rows each, two tiles either way, and 48 + 32 rows are faster than 64 + 16:
+// one sequence of 2048 latents 11.7 us against 12.5; longer runs of tiles are not: 64
+// sequences (320 rows a CTA) 18.4 us against 17.4, 200 of up to 640 rows 39.4 against 38.2.
 constexpr int kQ = 0;                              // 8 atoms x 64 heads x 128 B
 constexpr uint32_t kQBytes = kHeads * kLatent * 2;
 constexpr int kP = kQ + static_cast<int>(kQBytes); // 64 heads x 64 rows bf16
 constexpr int kPBytes = kHeads * 128;
-constexpr int kKV = kP + kPBytes;                  // the two slots
-constexpr int kKVBytes = kSlots * kSlotBytes;
-constexpr int kIds = kKV + kKVBytes;               // compacted latent rows
-constexpr int kMl = kIds + kMaxKTokens * 4;        // [8][64] (max, sum) of each CTA's rows
-constexpr int kMisc = kMl + kMaxAttnSplits * kHeads * 8;
+constexpr int kKV = kP + kPBytes;                  // the slots
 constexpr int kMiscBytes = 2048;
-constexpr int kSmemBytes = kMisc + kMiscBytes + 1024;  // + alignment slack of the base
-static_assert(kSmemBytes <= 227 * 1024 && kIds % 16 == 0 && kMisc % 16 == 0, "shared memory");
+template <int ROWS>
+struct Shape {
+  static_assert(ROWS == 64 || ROWS == 48, "tile rows");
+  static constexpr int kSlots = ROWS == 64 ? 2 : 3;
+  static constexpr int kWarpRows = ROWS / kLoadWarps;       // a loader warp's rows of a tile
+  static constexpr int kAtomBytes = ROWS * 128;             // 64 dims of a tile's rows
+  static constexpr int kSlotBytes = 8 * kAtomBytes;
+  static constexpr int kKVBytes = kSlots * kSlotBytes;
+  static constexpr int kIds = kKV + kKVBytes;               // compacted latent rows
+  static constexpr int kMl = kIds + kMaxKTokens * 4;        // [8][64] (max, sum) of each CTA
+  static constexpr int kMisc = kMl + kMaxAttnSplits * kHeads * 8;
+  static constexpr int kSmemBytes = kMisc + kMiscBytes + 1024;  // + alignment slack of the base
+  static_assert(kSmemBytes <= 227 * 1024 && kIds % 16 == 0 && kMisc % 16 == 0, "shared memory");
+  static_assert(kIds + (kN - ROWS) * 128 <= kSmemBytes, "the last atom is read past its rows");
+};
+constexpr int kMaxSlots = 3;
 constexpr int kTmemCols = 512;  // S[b]: cols [32 b, 32 b + 32); O^T slice m: [kTmemO + 64 m, ...)
 constexpr int kTmemO = 64;
 
@@ -74,12 +87,13 @@ constexpr int kTmemO = 64;
 // 8 u .. 8 u + 7 for each dim, plane 8 + u the next 8 bits of heads 16 u ..
 // 16 u + 15, so that a warp (32 dims) writes and reads 512 contiguous bytes.
 __host__ __device__ constexpr int xchg_bytes(int S) { return (kLatent / S) * 192; }
-static_assert(2 * xchg_bytes(2) <= kKVBytes && 4 * xchg_bytes(4) <= kKVBytes &&
-                  kMaxAttnSplits * xchg_bytes(kMaxAttnSplits) <= kKVBytes,
+static_assert(2 * xchg_bytes(2) <= Shape<64>::kKVBytes && 4 * xchg_bytes(4) <= Shape<64>::kKVBytes &&
+                  kMaxAttnSplits * xchg_bytes(kMaxAttnSplits) <= Shape<64>::kKVBytes &&
+                  Shape<64>::kKVBytes <= Shape<48>::kKVBytes,
               "receive areas fit the slots");
 
 struct Misc {
-  uint64_t kv_full[kSlots], kv_empty[kSlots], s_full[2], s_free[2], p_full, p_empty;
+  uint64_t kv_full[kMaxSlots], kv_empty[kMaxSlots], s_full[2], s_free[2], p_full, p_empty;
   uint64_t q_done, ids_ready;
   uint64_t o_done;  // every MMA of the CTA has completed
   uint32_t tmem_base;
@@ -172,8 +186,13 @@ __device__ __forceinline__ void stage_heads(uint32_t image, uint32_t row, int h0
   }
 }
 
+template <int ROWS>
 __global__ void __launch_bounds__(kThreads, 1)
     attn4_kernel(AttnArgs a, const __grid_constant__ CUtensorMap qmap) {
+  using TS = Shape<ROWS>;
+  constexpr int kRows = ROWS, kSlots = TS::kSlots, kWarpRows = TS::kWarpRows;
+  constexpr int kAtomBytes = TS::kAtomBytes, kSlotBytes = TS::kSlotBytes;
+  constexpr int kIds = TS::kIds, kMl = TS::kMl, kMisc = TS::kMisc;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -301,8 +320,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= kLoadWarp0 && warp < kMmaWarp) {
     // ---------------- loaders ----------------
-    // Loader warp w fills rows [8 w, 8 w + 8) of every tile, two rows at a
-    // time: lane l reads bytes [16 j, 16 j + 16) of row 8 w + 2 i + l / 16,
+    // Loader warp w fills rows [R w, R w + R) of every tile, R = kWarpRows, two at a
+    // time: lane l reads bytes [16 j, 16 j + 16) of row R w + 2 i + l / 16,
     // j = l % 16, which are its elements [32 j, 32 j + 32) under scale j. As soon as
     // a pair of rows is converted, the same pair of the next tile is read into the
     // same registers, so a tile's reads have the time of a tile to arrive. One copy
@@ -336,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (have_ids) read = next < n_tiles;
       if (!conv && !read) break;
-      // Lane r < 8 finds the source of row 8 w + r: its byte offset, or -1; bit 62
+      // Lane r < R finds the source of row R w + r: its byte offset, or -1; bit 62
       // marks the window.
       int64_t src_l = -1;
       if (read) {
@@ -444,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (n_tiles > 0) mma_commit_warp(leader, &misc->o_done);  // every MMA has completed
     } else {
-      constexpr uint32_t idesc_s = mma_idesc(kHeads, kRows, true, false, false);
+      constexpr uint32_t idesc_s = mma_idesc(kHeads, kN, true, false, false);
       bool qk_ok = n_tiles == 0 || wait_bar(&misc->q_done, 0u, misc, a.status);
       for (int t = 0; t < n_tiles && qk_ok; ++t) {
         const int sl = t % kSlots, sb = t & 1;
@@ -498,10 +517,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait_pv = [&](int t) {
       if (ok) ok = wait_bar(&misc->p_empty, static_cast<uint32_t>(t & 1), misc, a.status);
     };
-    constexpr int kHalf = kRows / 2;
     for (int t = 0; t < n_tiles; ++t) {
       const int sb = t & 1;
-      const int valid = n_rows_cta - t * kRows - kHalf * half;
+      const int valid = min(kRows, n_rows_cta - t * kRows) - kHalf * half;
       float z[kHalf];
       float mt = -INFINITY, alpha = 1.f;
       if (ok) ok = wait_bar(&misc->s_full[sb], static_cast<uint32_t>((t >> 1) & 1), misc, a.status);
@@ -779,6 +797,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
+namespace {
+
+template <int ROWS>
+cudaError_t launch_rows(const AttnArgs& a, const CUtensorMap& qmap, cudaStream_t s) {
+  static std::atomic<int> smem_set[64]{};
+  constexpr int smem = Shape<ROWS>::kSmemBytes;
+  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(attn4_kernel<ROWS>), smem, smem_set);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attn4_kernel<ROWS>, dim3(a.B, a.splits), dim3(kThreads), smem, s, a.splits, a,
+                    qmap);
+}
+
+}  // namespace
+
 cudaError_t launch_attn4(const AttnArgs& a, cudaStream_t s) {
   if (a.B == 0) return cudaSuccess;
   if (a.prefill || (a.splits != 1 && a.splits != 2 && a.splits != 4 && a.splits != 8)) {
@@ -786,16 +818,12 @@ cudaError_t launch_attn4(const AttnArgs& a, cudaStream_t s) {
   }
   CUtensorMap qmap;
   memset(&qmap, 0, sizeof(qmap));
-  cudaError_t e = encode_tma_2d(&qmap, a.q, 2, kLatent, static_cast<uint64_t>(a.B) * kHeads,
-                                kLatent * 2, 64, kHeads);
+  const cudaError_t e = encode_tma_2d(&qmap, a.q, 2, kLatent, static_cast<uint64_t>(a.B) * kHeads,
+                                      kLatent * 2, 64, kHeads);
   if (e != cudaSuccess) return e;
   AttnArgs args = a;
   args.swa_rows = static_cast<int64_t>(a.B) * a.window;
-  static std::atomic<int> smem_set[64]{};
-  e = ensure_smem(reinterpret_cast<const void*>(attn4_kernel), kSmemBytes, smem_set);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(attn4_kernel, dim3(a.B, a.splits), dim3(kThreads), kSmemBytes, s, a.splits,
-                    args, qmap);
+  return a.splits == 8 ? launch_rows<48>(args, qmap, s) : launch_rows<64>(args, qmap, s);
 }
 
 }  // namespace dsa
