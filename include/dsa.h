@@ -508,8 +508,9 @@ typedef enum { DSA_DT_BF16 = 0, DSA_DT_F16 = 1, DSA_DT_F32 = 2 } dsa_dtype_t;
 
 /* A group of heads: token t's head h has elements x[t * x_token_stride + h *
  * x_head_stride + 0 .. dim - 1], and goes to out by out's strides. Strides count
- * elements and, like the base pointers, are multiples of 16 bytes. out may be
- * x with the same strides (in place); they must not overlap otherwise. */
+ * elements and, like the base pointers, are multiples of 16 bytes; out's are at
+ * least dim. out may be x with the same strides (in place); they must not overlap
+ * otherwise, nor may out's heads. */
 typedef struct {
   const void* x;
   void* out;

@@ -111,6 +111,9 @@ def test_norm_rope_argument_errors(lib):
     assert call(out_head_stride=132) == 2
     assert call(dt=2, x_head_stride=130) == 2
     assert call(out_token_stride=512) == 1         # in place with other strides
+    assert call(x=2 * A, out_head_stride=0) == 1   # heads written over one another
+    assert call(x=2 * A, out_token_stride=120) == 1
+    assert call(x=2 * A, out_head_stride=-128) == 1
     assert call(eps=-1.0) == 1
     assert call(eps=float("nan")) == 1
     assert call(eps=float("inf")) == 1

@@ -1095,6 +1095,10 @@ dsa_status_t dsa_norm_rope(int n, const int32_t* n_valid, const int32_t* positio
         h.out_head_stride % elems) {
       return DSA_ERR_MISALIGNED;
     }
+    // no two heads may be written to one place
+    if ((h.heads > 1 && h.out_head_stride < h.dim) || (n > 1 && h.out_token_stride < h.dim)) {
+      return DSA_ERR_INVALID_ARG;
+    }
     if (h.x == h.out &&
         (h.x_token_stride != h.out_token_stride || h.x_head_stride != h.out_head_stride)) {
       return DSA_ERR_INVALID_ARG;
