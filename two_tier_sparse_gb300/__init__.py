@@ -336,15 +336,13 @@ def sparse_attn_prefill(cfg, ctx_len, q, q_idx, w, latents, keys: Keys, pooled: 
 def _launch_stream(t: torch.Tensor, stream):
     """The raw stream to launch on: the given one, or the current stream of t's
     device, which has to be the current device (the library launches there)."""
-    dev = t.get_device()
-    if dev != _current_device():
-        raise ValueError(f"tensors on device {dev}, but the current device is {_current_device()}")
+    dev = t.get_device()  # -1: on the host
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors on {t.device}, which is not the current CUDA device")
     return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
-def _i32(name, t, shape=None, optional=False):
-    if t is None and optional:
-        return
+def _i32(name, t, shape=None):
     if t.dtype != torch.int32 or not t.is_contiguous() or (shape is not None
                                                            and tuple(t.shape) != shape):
         raise ValueError(f"{name}: a contiguous int32 tensor"
@@ -370,6 +368,7 @@ class PagePool:
                 raise ValueError("ring_state: two int64 values")
         self.table, self.page_rows, self.free_ring = table, page_rows, free_ring
         self.ring_state, self.ring_state_out = ring_state, out
+        self.B = table.shape[0]
         self.c = _PagePool(table.data_ptr(), page_rows, table.shape[1], free_ring.shape[0],
                            free_ring.data_ptr(), ring_state.data_ptr(), out.data_ptr())
         self._ref = ctypes.byref(self.c)
@@ -400,7 +399,7 @@ class StepPlan:
                            ("latent_slots", latent_slots, m), ("window_slots", window_slots, m)):
             _i32(name, t, (n,))
             setattr(self, name, t)
-        self.max_new = m
+        self.B, self.max_new, self.shape = B, m, n_tokens.shape
         self.c = _StepPlan(n_tokens.data_ptr(), n_latents.data_ptr(), swa_len.data_ptr(),
                            cu_new.data_ptr(), token_seq.data_ptr(), positions.data_ptr(),
                            latent_slots.data_ptr(), window_slots.data_ptr(), m)
@@ -423,9 +422,9 @@ class StepPlan:
 def plan_step(cfg, n_tokens, n_new, pool: PagePool, plan: StepPlan, ws, stream=None):
     """Block table and slot maps of a step (dsa_plan_step): n_tokens [B] lengths
     before the step, n_new [B] tokens added (negative: the request ends)."""
-    B = plan.n_tokens.shape[0]
-    if n_tokens.dtype != torch.int32 or n_new.dtype != torch.int32 or n_tokens.shape != (B,) or \
-            n_new.shape != (B,) or pool.table.shape[0] != B or \
+    B, i32 = plan.B, torch.int32
+    if n_tokens.dtype is not i32 or n_new.dtype is not i32 or n_tokens.shape != plan.shape or \
+            n_new.shape != plan.shape or pool.B != B or \
             not (n_tokens.is_contiguous() and n_new.is_contiguous()):
         raise ValueError(f"n_tokens and n_new: contiguous int32 tensors of the plan's {B} requests, "
                          f"the pool's table a row for each")
@@ -480,6 +479,7 @@ class HeadSet:
             raise ValueError("groups of one element type, token count and device")
         self.groups = groups
         self.n, self.dtype = groups[0].n, groups[0].dtype
+        self.x, self.shape, self.count = groups[0].x, groups[0].x.shape[:1], len(groups)
         self._c = (_HeadsC * len(groups))(*[g.c for g in groups])
 
 
@@ -501,14 +501,15 @@ def norm_rope(positions, heads: HeadSet, rope: Optional[Rope] = None, n_valid=No
     [n]; n_valid: device int32 [1], tokens behind it are left as they were."""
     n = heads.n
     if rope is not None or positions is not None:
-        if positions is None or positions.dtype != torch.int32 or positions.shape != (n,) or \
-                not positions.is_contiguous():
+        if positions is None or positions.dtype is not torch.int32 or \
+                positions.shape != heads.shape or not positions.is_contiguous():
             raise ValueError(f"positions: contiguous int32 [{n}]")
-    _i32("n_valid", n_valid, (1,), optional=True)
+    if n_valid is not None:
+        _i32("n_valid", n_valid, (1,))
     code = load().dsa_norm_rope(n, None if n_valid is None else n_valid.data_ptr(),
                                 None if positions is None else positions.data_ptr(), heads.dtype,
-                                heads._c, len(heads._c), None if rope is None else rope._ref,
-                                _launch_stream(heads.groups[0].x, stream))
+                                heads._c, heads.count, None if rope is None else rope._ref,
+                                _launch_stream(heads.x, stream))
     if code:
         raise DsaError(code, "dsa_norm_rope")
 

@@ -356,12 +356,18 @@ cudaError_t launch_nv(NormRopeArgs a, cudaStream_t s) {
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(norm_rope_kernel<T, NV>), smem, smem_set);
   if (e != cudaSuccess) return e;
   // As many CTAs as the SMs hold at once, or one for every eight units of fewer.
-  int per_sm = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, norm_rope_kernel<T, NV>, 32 * kWarps,
-                                                    static_cast<size_t>(smem)) != cudaSuccess ||
-      per_sm < 1) {
-    cudaGetLastError();  // clear the error the failed query left behind
-    per_sm = 1;
+  // (The last answer is kept with the shared memory it is for, in one word.)
+  static std::atomic<int64_t> last{0};
+  const int64_t known = last.load(std::memory_order_relaxed);
+  int per_sm = static_cast<int>(known & 0xFFFF);
+  if (known >> 16 != smem + 1) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, norm_rope_kernel<T, NV>, 32 * kWarps,
+                                                      static_cast<size_t>(smem)) != cudaSuccess ||
+        per_sm < 1) {
+      cudaGetLastError();  // clear the error the failed query left behind
+      per_sm = 1;
+    }
+    last.store((int64_t{smem} + 1) << 16 | per_sm, std::memory_order_relaxed);
   }
   const int64_t want = (static_cast<int64_t>(a.n) * a.units + kWarps - 1) / kWarps;
   const int grid = static_cast<int>(std::min<int64_t>(want, int64_t{per_sm} * device_sm_count()));
