@@ -38,8 +38,9 @@ namespace dsa {
 
 namespace {
 
-constexpr int kN = 64;                             // rows of a QK^T MMA
-constexpr int kHalf = kN / 2;                      // scores of a math thread
+constexpr int kRows = 64;                          // rows of a tile
+constexpr int kHalf = kRows / 2;                   // scores of a math thread
+constexpr int kSlots = 2;
 constexpr int kLoadWarp0 = 4;
 constexpr int kLoadWarps = 8;
 constexpr int kMmaWarp = kLoadWarp0 + kLoadWarps;  // 12: QK^T issuer (and TMEM owner)
@@ -50,35 +51,21 @@ constexpr int kEpiBar = 2;                         // of the epilogue (math and 
 constexpr int kEpiThreads = 32 * kMmaWarp;         // 384
 constexpr int kEpiGroups = kEpiThreads / 128;      // 3 groups of four warps (TMEM lane quarters)
 
-// Tiles of ROWS rows and the shared memory they make, offsets from a 1024-aligned base.
-// Two slots of 64 rows, or three of 48: with three, loads, softmax and MMAs of more tiles
-// overlap, but a QK^T step still takes the time of 64 rows (it reads 16 rows past each
-// atom, into what follows, and their scores are not used). A cluster of eight CTAs has
-// at most 80 rows each, two tiles either way, and 48 + 32 rows are faster than 64 + 16:
-// one sequence of 2048 latents 11.7 us against 12.5; longer runs of tiles are not: 64
-// sequences (320 rows a CTA) 18.4 us against 17.4, 200 of up to 640 rows 39.4 against 38.2.
+// Shared memory, offsets from a 1024-aligned base.
+constexpr int kAtomBytes = kRows * 128;            // 64 dims of a tile's rows
+constexpr int kSlotBytes = 8 * kAtomBytes;
 constexpr int kQ = 0;                              // 8 atoms x 64 heads x 128 B
 constexpr uint32_t kQBytes = kHeads * kLatent * 2;
 constexpr int kP = kQ + static_cast<int>(kQBytes); // 64 heads x 64 rows bf16
 constexpr int kPBytes = kHeads * 128;
-constexpr int kKV = kP + kPBytes;                  // the slots
+constexpr int kKV = kP + kPBytes;                  // the two slots
+constexpr int kKVBytes = kSlots * kSlotBytes;
+constexpr int kIds = kKV + kKVBytes;               // compacted latent rows
+constexpr int kMl = kIds + kMaxKTokens * 4;        // [8][64] (max, sum) of each CTA's rows
+constexpr int kMisc = kMl + kMaxAttnSplits * kHeads * 8;
 constexpr int kMiscBytes = 2048;
-template <int ROWS>
-struct Shape {
-  static_assert(ROWS == 64 || ROWS == 48, "tile rows");
-  static constexpr int kSlots = ROWS == 64 ? 2 : 3;
-  static constexpr int kWarpRows = ROWS / kLoadWarps;       // a loader warp's rows of a tile
-  static constexpr int kAtomBytes = ROWS * 128;             // 64 dims of a tile's rows
-  static constexpr int kSlotBytes = 8 * kAtomBytes;
-  static constexpr int kKVBytes = kSlots * kSlotBytes;
-  static constexpr int kIds = kKV + kKVBytes;               // compacted latent rows
-  static constexpr int kMl = kIds + kMaxKTokens * 4;        // [8][64] (max, sum) of each CTA
-  static constexpr int kMisc = kMl + kMaxAttnSplits * kHeads * 8;
-  static constexpr int kSmemBytes = kMisc + kMiscBytes + 1024;  // + alignment slack of the base
-  static_assert(kSmemBytes <= 227 * 1024 && kIds % 16 == 0 && kMisc % 16 == 0, "shared memory");
-  static_assert(kIds + (kN - ROWS) * 128 <= kSmemBytes, "the last atom is read past its rows");
-};
-constexpr int kMaxSlots = 3;
+constexpr int kSmemBytes = kMisc + kMiscBytes + 1024;  // + alignment slack of the base
+static_assert(kSmemBytes <= 227 * 1024 && kIds % 16 == 0 && kMisc % 16 == 0, "shared memory");
 constexpr int kTmemCols = 512;  // S[b]: cols [32 b, 32 b + 32); O^T slice m: [kTmemO + 64 m, ...)
 constexpr int kTmemO = 64;
 
@@ -87,13 +74,12 @@ constexpr int kTmemO = 64;
 // 8 u .. 8 u + 7 for each dim, plane 8 + u the next 8 bits of heads 16 u ..
 // 16 u + 15, so that a warp (32 dims) writes and reads 512 contiguous bytes.
 __host__ __device__ constexpr int xchg_bytes(int S) { return (kLatent / S) * 192; }
-static_assert(2 * xchg_bytes(2) <= Shape<64>::kKVBytes && 4 * xchg_bytes(4) <= Shape<64>::kKVBytes &&
-                  kMaxAttnSplits * xchg_bytes(kMaxAttnSplits) <= Shape<64>::kKVBytes &&
-                  Shape<64>::kKVBytes <= Shape<48>::kKVBytes,
+static_assert(2 * xchg_bytes(2) <= kKVBytes && 4 * xchg_bytes(4) <= kKVBytes &&
+                  kMaxAttnSplits * xchg_bytes(kMaxAttnSplits) <= kKVBytes,
               "receive areas fit the slots");
 
 struct Misc {
-  uint64_t kv_full[kMaxSlots], kv_empty[kMaxSlots], s_full[2], s_free[2], p_full, p_empty;
+  uint64_t kv_full[kSlots], kv_empty[kSlots], s_full[2], s_free[2], p_full, p_empty;
   uint64_t q_done, ids_ready;
   uint64_t o_done;  // every MMA of the CTA has completed
   uint32_t tmem_base;
@@ -186,13 +172,8 @@ __device__ __forceinline__ void stage_heads(uint32_t image, uint32_t row, int h0
   }
 }
 
-template <int ROWS>
 __global__ void __launch_bounds__(kThreads, 1)
     attn4_kernel(AttnArgs a, const __grid_constant__ CUtensorMap qmap) {
-  using TS = Shape<ROWS>;
-  constexpr int kRows = ROWS, kSlots = TS::kSlots, kWarpRows = TS::kWarpRows;
-  constexpr int kAtomBytes = TS::kAtomBytes, kSlotBytes = TS::kSlotBytes;
-  constexpr int kIds = TS::kIds, kMl = TS::kMl, kMisc = TS::kMisc;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -320,21 +301,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= kLoadWarp0 && warp < kMmaWarp) {
     // ---------------- loaders ----------------
-    // Loader warp w fills rows [R w, R w + R) of every tile, R = kWarpRows, two at a
-    // time: lane l reads bytes [16 j, 16 j + 16) of row R w + 2 i + l / 16,
-    // j = l % 16, which are its elements [32 j, 32 j + 32) under scale j. As soon as
-    // a pair of rows is converted, the same pair of the next tile is read into the
-    // same registers, so a tile's reads have the time of a tile to arrive. One copy
-    // of the code does every pass (the first only reads, the last only converts).
-    // Rows without a source are zeros.
+    // Loader warp w fills rows [8 w, 8 w + 8) of every tile. Lane l has row 8 w + r, r = l % 8,
+    // and of it the 16-byte pieces g, g + 4, g + 8 and g + 12, g = l / 8: elements
+    // [32 j, 32 j + 32) under scale j for piece j. The eight lanes of a 16-byte store then write
+    // one chunk of eight different rows, which the swizzle spreads over all banks,
+    // and every address is a lane's constant. The next tile's pieces are read into the
+    // registers as soon as this tile's are converted; one copy of the code does every pass (the first only reads, the last only
+    // converts). Rows without a source are zeros.
     const int w = warp - kLoadWarp0;
-    const int j = lane & 15, half = lane >> 4;
+    const uint32_t r = lane & 7, g = lane >> 3;
     const uint8_t* lat = reinterpret_cast<const uint8_t*>(a.latents);
     const uint8_t* swa = reinterpret_cast<const uint8_t*>(a.swa);
     bool have_ids = false;
     int s_begin = 0, n_rows_cta = w_cnt, n_tiles = 0;
-    uint4 code[kWarpRows / 2];
-    uint32_t scale[kWarpRows / 2];
+    uint32_t to[4];  // where word n of piece g goes in a slot (piece g + 4 i: two atoms on each)
+#pragma unroll
+    for (uint32_t n = 0; n < 4; ++n) {
+      to[n] = sbase + kKV + (g >> 1) * kAtomBytes + (8u * w + r) * 128u +
+              (((4u * (g & 1u) + n) ^ r) << 4);
+    }
+    uint4 code[4], scales;
     int next = 0, done = 0;  // tiles read, tiles converted
     for (;;) {
       const bool conv = next > done;
@@ -355,71 +341,57 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (have_ids) read = next < n_tiles;
       if (!conv && !read) break;
-      // Lane r < R finds the source of row R w + r: its byte offset, or -1; bit 62
-      // marks the window.
-      int64_t src_l = -1;
-      if (read) {
-        const int g = next * kRows + kWarpRows * w + lane;
-        if (lane < kWarpRows && g < n_rows_cta) {
-          if (g < w_cnt) {
-            const int64_t row = wrow0 + w_begin + g;
-            if (DSA_DCHECK(row >= 0 && row < a.swa_rows, a.status, SITE_ATTN, row)) {
-              src_l = row * kRow4Bytes | (int64_t{1} << 62);
-            }
-          } else {
-            const int64_t row = lat_row0 + ids[s_begin + g - w_cnt];
-            if (DSA_DCHECK(row >= 0 && row < a.lat_rows, a.status, SITE_ATTN, row)) {
-              src_l = row * kRow4Bytes;
-            }
+      const uint8_t* src = nullptr;  // this lane's row of the next tile
+      const int row_g = next * kRows + 8 * w + static_cast<int>(r);
+      if (read && row_g < n_rows_cta) {
+        if (row_g < w_cnt) {
+          const int64_t row = wrow0 + w_begin + row_g;
+          if (DSA_DCHECK(row >= 0 && row < a.swa_rows, a.status, SITE_ATTN, row)) {
+            src = swa + row * kRow4Bytes;
           }
-        }
-      }
-      const int sl = done % kSlots;
-      if (conv && done >= kSlots &&
-          !wait_bar(&misc->kv_empty[sl], static_cast<uint32_t>(((done / kSlots) - 1) & 1), misc,
-                    a.status)) {
-        ok = false;
-        break;
-      }
-      // Word i of the 16 bytes is 16-byte chunk 4 (j & 1) + i of the row in
-      // atom j / 2. The order is rotated by atom so that eight lanes (four
-      // atoms, both halves) write eight different 16-byte bank groups.
-      const int rot = (j >> 1) & 3;
-      const uint32_t base = sbase + kKV + sl * kSlotBytes +
-                            static_cast<uint32_t>(j >> 1) * kAtomBytes;
-#pragma unroll
-      for (int i = 0; i < kWarpRows / 2; ++i) {
-        if (conv) {
-          uint4 c = code[i];
-          if (rot & 1) c = make_uint4(c.y, c.z, c.w, c.x);
-          if (rot & 2) c = make_uint4(c.z, c.w, c.x, c.y);
-          const uint32_t f = mx4_scale_bf16x2(scale[i]);
-          const uint32_t row = static_cast<uint32_t>(kWarpRows * w + 2 * i + half);
-          const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            const uint32_t chunk = 4u * (j & 1) + ((n + rot) & 3);
-            st_shared_v4(base + sw128_off(row, chunk), mx4_decode8(cw[n], f));
-          }
-        }
-        if (read) {
-          const int64_t src = __shfl_sync(0xFFFFFFFFu, src_l, 2 * i + half);
-          code[i] = make_uint4(0u, 0u, 0u, 0u);
-          scale[i] = 0u;
-          if (src >= 0) {
-            const uint8_t* p = (src >> 62 ? swa : lat) + (src & ~(int64_t{1} << 62));
-            code[i] = __ldg(reinterpret_cast<const uint4*>(p) + j);
-            scale[i] = __ldg(p + kRow4Codes + j);
+        } else {
+          const int64_t row = lat_row0 + ids[s_begin + row_g - w_cnt];
+          if (DSA_DCHECK(row >= 0 && row < a.lat_rows, a.status, SITE_ATTN, row)) {
+            src = lat + row * kRow4Bytes;
           }
         }
       }
       if (conv) {
+        const int sl = done % kSlots;
+        if (done >= kSlots &&
+            !wait_bar(&misc->kv_empty[sl], static_cast<uint32_t>(((done / kSlots) - 1) & 1), misc,
+                      a.status)) {
+          ok = false;
+          break;
+        }
+        const uint32_t slot = static_cast<uint32_t>(sl * kSlotBytes);
+        const uint32_t sw[4] = {scales.x, scales.y, scales.z, scales.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // piece g + 4 i: its scale is byte g of word i
+          const uint32_t f = mx4_scale_bf16x2((sw[i] >> (8u * g)) & 0xFFu);
+          const uint32_t cw[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            st_shared_v4(to[n] + slot + 2 * i * kAtomBytes, mx4_decode8(cw[n], f));
+          }
+        }
         fence_proxy_async_smem();  // the MMAs read the tile through the async proxy
         __syncwarp();
         if (lane == 0) mbar_arrive(&misc->kv_full[sl]);
         ++done;
       }
-      if (read) ++next;
+      if (read) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) code[i] = make_uint4(0u, 0u, 0u, 0u);
+        scales = make_uint4(0u, 0u, 0u, 0u);
+        if (src != nullptr) {
+          const uint4* p = reinterpret_cast<const uint4*>(src);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) code[i] = __ldg(p + g + 4 * i);
+          scales = __ldg(p + kRow4Codes / 16);
+        }
+        ++next;
+      }
     }
     n_tiles_e = have_ids ? n_tiles : 0;
   } else if (warp == kMmaWarp || warp == kPvWarp) {
@@ -463,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (n_tiles > 0) mma_commit_warp(leader, &misc->o_done);  // every MMA has completed
     } else {
-      constexpr uint32_t idesc_s = mma_idesc(kHeads, kN, true, false, false);
+      constexpr uint32_t idesc_s = mma_idesc(kHeads, kRows, true, false, false);
       bool qk_ok = n_tiles == 0 || wait_bar(&misc->q_done, 0u, misc, a.status);
       for (int t = 0; t < n_tiles && qk_ok; ++t) {
         const int sl = t % kSlots, sb = t & 1;
@@ -519,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     for (int t = 0; t < n_tiles; ++t) {
       const int sb = t & 1;
-      const int valid = min(kRows, n_rows_cta - t * kRows) - kHalf * half;
+      const int valid = n_rows_cta - t * kRows - kHalf * half;
       float z[kHalf];
       float mt = -INFINITY, alpha = 1.f;
       if (ok) ok = wait_bar(&misc->s_full[sb], static_cast<uint32_t>((t >> 1) & 1), misc, a.status);
@@ -797,20 +769,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-namespace {
-
-template <int ROWS>
-cudaError_t launch_rows(const AttnArgs& a, const CUtensorMap& qmap, cudaStream_t s) {
-  static std::atomic<int> smem_set[64]{};
-  constexpr int smem = Shape<ROWS>::kSmemBytes;
-  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(attn4_kernel<ROWS>), smem, smem_set);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(attn4_kernel<ROWS>, dim3(a.B, a.splits), dim3(kThreads), smem, s, a.splits, a,
-                    qmap);
-}
-
-}  // namespace
-
 cudaError_t launch_attn4(const AttnArgs& a, cudaStream_t s) {
   if (a.B == 0) return cudaSuccess;
   if (a.prefill || (a.splits != 1 && a.splits != 2 && a.splits != 4 && a.splits != 8)) {
@@ -818,12 +776,16 @@ cudaError_t launch_attn4(const AttnArgs& a, cudaStream_t s) {
   }
   CUtensorMap qmap;
   memset(&qmap, 0, sizeof(qmap));
-  const cudaError_t e = encode_tma_2d(&qmap, a.q, 2, kLatent, static_cast<uint64_t>(a.B) * kHeads,
-                                      kLatent * 2, 64, kHeads);
+  cudaError_t e = encode_tma_2d(&qmap, a.q, 2, kLatent, static_cast<uint64_t>(a.B) * kHeads,
+                                kLatent * 2, 64, kHeads);
   if (e != cudaSuccess) return e;
   AttnArgs args = a;
   args.swa_rows = static_cast<int64_t>(a.B) * a.window;
-  return a.splits == 8 ? launch_rows<48>(args, qmap, s) : launch_rows<64>(args, qmap, s);
+  static std::atomic<int> smem_set[64]{};
+  e = ensure_smem(reinterpret_cast<const void*>(attn4_kernel), kSmemBytes, smem_set);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attn4_kernel, dim3(a.B, a.splits), dim3(kThreads), kSmemBytes, s, a.splits,
+                    args, qmap);
 }
 
 }  // namespace dsa
