@@ -482,3 +482,29 @@ def test_tensors_of_another_device_are_refused():
         dsa.norm_rope(None, dsa.HeadSet([dsa.Heads(x)]))
     with pytest.raises(ValueError):
         dsa.kv_write(dsa.config(), x, torch.zeros(2, dtype=torch.int32), x, small_ws())
+
+
+def test_a_row_written_right_before_the_attention_is_read():
+    """kv_write -> sparse_attn_decode with nothing between: many times over, every output
+    that of the row just written (one visible row, so the output is the row)."""
+    for fmt in (dsa.KV_BF16, dsa.KV_MXFP4):
+        cfg = dsa.config(kv_fmt=fmt, window=4, k_tokens=8, k_blocks=8)
+        ws = dsa.workspace(cfg, 1, 64)
+        row = {dsa.KV_BF16: 512, dsa.KV_MXFP4: 272}[fmt]
+        swa = torch.zeros((1, 4, row), device="cuda",
+                          dtype=torch.bfloat16 if fmt == dsa.KV_BF16 else torch.uint8)
+        lat = torch.zeros((1, 64, row), device="cuda", dtype=swa.dtype)
+        q = torch.zeros((1, 64, 512), dtype=torch.bfloat16, device="cuda")
+        zero, one = (torch.full((1,), v, dtype=torch.int32, device="cuda") for v in (0, 1))
+        ids = torch.full((1, 8), -1, dtype=torch.int32, device="cuda")
+        outs = [torch.empty((1, 64, 512), dtype=torch.bfloat16, device="cuda") for _ in range(60)]
+        rows = [torch.full((1, 512), float(1 << (i % 8)), dtype=torch.bfloat16, device="cuda")
+                for i in range(60)]
+        torch.cuda.synchronize()
+        for r, o in zip(rows, outs):
+            dsa.kv_write(cfg, r, zero, swa, ws)
+            dsa.sparse_attn_decode(cfg, q, lat, zero, ids, swa, one, o, ws)
+        torch.cuda.synchronize()
+        for r, o in zip(rows, outs):
+            assert (o == r[0, 0]).all()
+        assert dsa.read_device_status(ws)[0] == 0

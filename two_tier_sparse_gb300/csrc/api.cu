@@ -643,6 +643,7 @@ dsa_status_t attn_decode(const dsa_config_t* cfg, const void* q, const void* lat
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
   a.status = at<DeviceStatus>(workspace, L.status);
+  a.wait_first = 1;
   set_splits(a, *cfg, B);
   Range range("dsa.attention");
   DSA_CUDA(launch(DSA_KERNEL_ATTN, static_cast<cudaStream_t>(stream), [&](int*) { return launch_decode_attn(a, *cfg, static_cast<cudaStream_t>(stream)); }));
@@ -770,6 +771,7 @@ dsa_status_t dsa_decode_step(const dsa_config_t* cfg, const void* q, const void*
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
   a.status = st;
+  a.wait_first = max_latents == 0;  // (no scan then)
   set_splits(a, *cfg, B);
   Range attn_range("dsa.attention");
   DSA_CUDA(launch(DSA_KERNEL_ATTN, s, [&](int*) { return launch_decode_attn(a, *cfg, s); }));
@@ -832,6 +834,7 @@ dsa_status_t dsa_sparse_attn_prefill(const dsa_config_t* cfg, int n_q, int64_t c
   a.ctx = ctx_len;
   a.ratio = cfg->ratio;
   a.status = st;
+  a.wait_first = n_lat == 0;
   set_splits(a, *cfg, n_q);
   Range attn_range("dsa.attention");
   DSA_CUDA(launch(DSA_KERNEL_ATTN, s, [&](int*) { return launch_attn(a, s); }));
@@ -900,6 +903,7 @@ dsa_status_t dsa_decode_multi(const dsa_config_t* cfg, int n_q, const int32_t* n
   a.n_tokens = n_tokens;
   a.swa_seq_rows = cfg->window + n_q - 1;
   a.status = st;
+  a.wait_first = max_latents == 0;
   set_splits(a, *cfg, nq_total);
   Range attn_range("dsa.attention");
   DSA_CUDA(launch(DSA_KERNEL_ATTN, s, [&](int*) { return launch_attn(a, s); }));

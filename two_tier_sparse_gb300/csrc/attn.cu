@@ -175,6 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();  // barriers initialised, tensor memory allocated
   tc_fence_after();
+  if (a.wait_first) griddep_wait();
   // The partner's barriers are initialised before any remote arrival: every
   // thread arrives here and waits before its first cluster access.
   if (paired) cluster_arrive_relaxed();
@@ -1037,6 +1038,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();  // barriers initialised, tensor memory allocated
   tc_fence_after();
+  if (a.wait_first) griddep_wait();
   const uint32_t tmem = misc->tmem_base;
 
   // Tile count of query index qi (its lists compacted): window rows + ids.

@@ -185,8 +185,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int split = blockIdx.y;  // rank in the cluster
   const int S = a.splits;
   const bool paired = S > 1;
-  int n_vis = a.n_latents[b];
-  int n_sw = a.swa_len[b];
+  int n_vis = 0, n_sw = 0;
+  if (!a.wait_first) {  // (on their way while the barriers are set up)
+    n_vis = a.n_latents[b];
+    n_sw = a.swa_len[b];
+  }
 
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
@@ -214,6 +217,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   // thread arrives here and waits before its first cluster access.
   if (paired) cluster_arrive_relaxed();
 
+  if (a.wait_first) {
+    griddep_wait();
+    n_vis = a.n_latents[b];
+    n_sw = a.swa_len[b];
+  }
   if (n_sw < 0 || n_sw > a.window) {
     if (tid == 0 && split == 0) report(a.status, static_cast<uint32_t>(b));
     n_sw = n_sw < 0 ? 0 : a.window;

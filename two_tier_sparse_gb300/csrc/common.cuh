@@ -259,6 +259,10 @@ __device__ __forceinline__ void fence_proxy_async_global() {
 // start its launch (griddep_launch_dependents) and waits for the previous
 // kernel's grid to finish and flush its memory (griddep_wait) before touching
 // global memory. Both are no-ops when the launch did not ask for it.
+// The attention reads queries, lengths and window rows ahead of its wait, while the
+// selection runs; so of the kernels before it in a call, one lets its dependents start
+// only once its own wait has returned (the tail pool, or else the scan): what came before
+// the call has then finished and is visible.
 // ---------------------------------------------------------------------------
 
 __device__ __forceinline__ void griddep_launch_dependents() {

@@ -268,6 +268,10 @@ struct AttnArgs {
   // code * kv_scale.
   int kv_fp8;
   float kv_scale;
+  // Nothing is read before the previous kernel has finished: a call of the attention alone,
+  // whose queries and window rows that kernel may have written. After a scan the previous
+  // kernels are the call's own, and they write the token ids only.
+  int wait_first;
   DeviceStatus* status;
 };
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s);

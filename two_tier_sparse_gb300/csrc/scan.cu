@@ -814,7 +814,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sbase = (raw + 1023u) & ~1023u;
   Shared& sh = *reinterpret_cast<Shared*>(smem_raw + (sbase - raw) + Lo::kShared);
   const int warp = threadIdx.x >> 5;
-  griddep_launch_dependents();
+  // (deferred: the tail pool before it has waited)
+  if (a.defer_wait) griddep_launch_dependents();
 
   const int64_t per = total / gridDim.x, rem = total % gridDim.x;
   const int64_t bx = blockIdx.x;
@@ -845,7 +846,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The previous kernel's outputs (scores, ids, pooled keys) are final past
   // this wait; with defer_wait only the producer takes it, before the tiles
   // that the tail pool writes (nothing else here reads a library output).
-  if (!a.defer_wait) griddep_wait();
+  if (!a.defer_wait) {
+    griddep_wait();
+    griddep_launch_dependents();
+  }
 
   if (warp < kMmaWarp) {
     producer<FMT, TPS>(a, maps, sh, sbase, t_begin, n_tiles, tpq, warp);

@@ -282,7 +282,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sbase = (raw + 1023u) & ~1023u;
   Shared& sh = *reinterpret_cast<Shared*>(smem_raw + (sbase - raw) + kShared);
   const int warp = threadIdx.x >> 5;
-  griddep_launch_dependents();
   const int64_t per = total / gridDim.x, rem = total % gridDim.x;
   const int64_t bx = blockIdx.x;
   const int64_t i0 = bx * per + (bx < rem ? bx : rem);
@@ -306,6 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   griddep_wait();  // the previous kernel's outputs (pooled keys, scores) are final
+  griddep_launch_dependents();
 
   if (warp == 0) {
     producer(a, maps, sh, sbase, i0, i1, T);
