@@ -508,9 +508,10 @@ typedef enum { DSA_DT_BF16 = 0, DSA_DT_F16 = 1, DSA_DT_F32 = 2 } dsa_dtype_t;
 
 /* A group of heads: token t's head h has elements x[t * x_token_stride + h *
  * x_head_stride + 0 .. dim - 1], and goes to out by out's strides. Strides count
- * elements and, like the base pointers, are multiples of 16 bytes; out's are at
- * least dim. out may be x with the same strides (in place); they must not overlap
- * otherwise, nor may out's heads. */
+ * elements and, like the base pointers, are multiples of 16 bytes; that of a single
+ * token or head is not used. out's heads do not overlap (DSA_ERR_INVALID_ARG). out may be
+ * x with the same strides (in place); they must not overlap otherwise, nor may two groups'
+ * outputs. */
 typedef struct {
   const void* x;
   void* out;

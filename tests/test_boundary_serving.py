@@ -208,3 +208,27 @@ def test_binding_refuses_what_it_cannot_pass(lib):
             dsa.kv_write(c, kw["rows"], kw["slots"], kw["cache"], None, n_valid=kw["n_valid"])
         with pytest.raises(ValueError):
             dsa.kv_read(c, kw["cache"], kw["slots"], kw["rows"], None, n_valid=kw["n_valid"])
+
+
+def test_heads_that_overlap_are_refused(lib):
+    """Distances of two heads: every pair of spans, from their strides."""
+    def call(heads, hs, n, ts, dim=128):
+        h = dsa._HeadsC(x=2 * A, out=A, heads=heads, dim=dim, x_token_stride=ts, x_head_stride=hs,
+                        out_token_stride=ts, out_head_stride=hs, weight=None, eps=0.0, norm=1,
+                        rope_start=-1)
+        return lib.dsa_norm_rope(n, None, None, 0, ctypes.byref(h), 1, None, None)
+    assert call(2, 128, 2, 128) == 1     # head 1 of a token is head 0 of the next
+    assert call(3, 256, 2, 256 + 64) == 1
+    assert call(5, 300 * 8, 7, 600 * 8 + 64) == 1
+    assert call(2, 1 << 62, 2, 128) == 1
+    assert call(2, 128, 2, 1 << 62) == 1
+    assert call(1, 129, 0, 129) == 0     # the stride of a single head or token is not used
+
+
+def test_serving_tensors_of_two_devices_are_refused(lib):
+    host, meta = torch.zeros(2, dtype=torch.int32), torch.zeros(2, dtype=torch.int32, device="meta")
+    state = torch.zeros(2, dtype=torch.int64)
+    with pytest.raises(ValueError):
+        dsa._one_device(host, None, type("T", (), dict(get_device=lambda s: 0, device="cuda:0"))())
+    dsa._one_device(host, None, meta)  # neither is on a CUDA device
+    dsa.PagePool(host.view(1, 2), 64, host, state)

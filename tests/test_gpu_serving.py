@@ -484,6 +484,96 @@ def test_tensors_of_another_device_are_refused():
         dsa.kv_write(dsa.config(), x, torch.zeros(2, dtype=torch.int32), x, small_ws())
 
 
+def test_calls_with_a_host_tensor_among_their_tensors_are_refused():
+    cfg, ws = dsa.config(), small_ws()
+
+    def host(t):
+        return t.cpu()
+    rows = torch.zeros((2, 512), dtype=torch.bfloat16, device="cuda")
+    slots = torch.zeros(2, dtype=torch.int32, device="cuda")
+    one = torch.ones(1, dtype=torch.int32, device="cuda")
+    cache = torch.zeros((4, 512), dtype=torch.bfloat16, device="cuda")
+    for bad in range(4):
+        a = [slots, cache, ws, one]
+        a[bad] = host(a[bad])
+        with pytest.raises(ValueError):
+            dsa.kv_write(cfg, rows, a[0], a[1], a[2], n_valid=a[3])
+        with pytest.raises(ValueError):
+            dsa.kv_read(cfg, a[1], a[0], rows, a[2], n_valid=a[3])
+    f = torch.ones(32, dtype=torch.float64, device="cuda")
+    for bad in range(3):
+        a = [slots, f, one]
+        a[bad] = host(a[bad])
+        with pytest.raises(ValueError):
+            dsa.norm_rope(a[0], dsa.HeadSet([dsa.Heads(rows, rope_start=0)]), dsa.Rope(a[1]),
+                          n_valid=a[2])
+    plan, pool = dsa.StepPlan.empty(2, 2), dsa.PagePool.empty(2, 64, 2, 4)
+    for bad in range(3):
+        a = [slots, slots, ws]
+        a[bad] = host(a[bad])
+        with pytest.raises(ValueError):
+            dsa.plan_step(cfg, a[0], a[1], pool, plan, a[2])
+    with pytest.raises(ValueError):
+        dsa.plan_step(cfg, slots, slots, dsa.PagePool.empty(2, 64, 2, 4, device="cpu"), plan, ws)
+    with pytest.raises(ValueError):
+        dsa.PagePool(pool.table, 64, host(pool.free_ring), pool.ring_state)
+    with pytest.raises(ValueError):
+        dsa.StepPlan(slots, slots, host(slots), torch.zeros(3, dtype=torch.int32, device="cuda"),
+                     one, one, one, one)
+
+
+@pytest.mark.parametrize("heads,n", [(1, 1), (1, 3), (2, 1), (2, 2), (3, 2), (2, 4), (3, 5)])
+def test_norm_rope_takes_every_layout_whose_heads_are_apart(heads, n):
+    """Strides from one element of 16 bytes on: refused when two heads share an element,
+    normed as they lie otherwise. dim 16, bf16, weights of one, eps 0."""
+    dim, step = 16, 8
+    gen = torch.Generator().manual_seed(100 * heads + n)
+    taken = refused = 0
+    for hs in range(step, 13 * step, step):
+        for ts in range(step, 13 * step, step):
+            at = [h * hs + t * ts for t in range(n) for h in range(heads)]
+            apart = all(abs(a - b) >= dim for i, a in enumerate(at) for b in at[:i])
+            x = torch.randn((max(at) + dim,), generator=gen).to(torch.bfloat16).cuda()
+            out = torch.full_like(x, 9.0)
+            h = dsa._HeadsC(x=x.data_ptr(), out=out.data_ptr(), heads=heads, dim=dim,
+                            x_token_stride=ts, x_head_stride=hs, out_token_stride=ts,
+                            out_head_stride=hs, weight=None, eps=0.0, norm=1, rope_start=-1)
+            import ctypes
+            code = dsa.load().dsa_norm_rope(n, None, None, 0, ctypes.byref(h), 1, None,
+                                            torch.cuda.current_stream().cuda_stream)
+            assert code == (0 if apart else 1), (hs, ts)
+            if not apart:
+                refused += 1
+                continue
+            taken += 1
+            want = torch.full(x.shape, 9.0, dtype=torch.float64)
+            tol = torch.zeros(x.shape, dtype=torch.float64)
+            xd = x.double().cpu()
+            for a in at:
+                v = xd[a:a + dim]
+                y = v / v.square().mean().sqrt()
+                want[a:a + dim] = y
+                tol[a:a + dim] = y.abs() * (2.0 ** -8 + 2.0 ** -19)
+            assert ((out.double().cpu() - want).abs() <= tol).all(), (hs, ts)
+    assert taken and (refused or heads * n == 1)
+
+
+def test_single_tokens_with_a_stride_of_any_size():
+    """The stride of a dimension of one is not used, whatever it is."""
+    big = torch.randn((4, 515), device="cuda").to(torch.bfloat16)
+    x = big[:1, :512]
+    assert x.stride(0) % 8
+    w = torch.ones(512, device="cuda")
+    out = torch.empty((1, 512), dtype=torch.bfloat16, device="cuda")
+    dsa.norm_rope(None, dsa.HeadSet([dsa.Heads(x, out, w, eps=0.0)]))
+    y = x.double() / x.double().square().mean().sqrt()
+    assert ((out.double() - y).abs() <= y.abs() * (2.0 ** -8 + 2.0 ** -19)).all()
+    cache = torch.zeros((2, 512), dtype=torch.bfloat16, device="cuda")
+    one = torch.ones(1, dtype=torch.int32, device="cuda")
+    dsa.kv_write(dsa.config(), x, one, cache, small_ws())
+    assert torch.equal(cache[1], x[0]) and not cache[0].any()
+
+
 def test_a_row_written_right_before_the_attention_is_read():
     """kv_write -> sparse_attn_decode with nothing between: many times over, every output
     that of the row just written (one visible row, so the output is the row)."""

@@ -342,6 +342,14 @@ def _launch_stream(t: torch.Tensor, stream):
     return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
+def _one_device(*tensors):
+    """Refuses tensors of different devices (None: not given)."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on {tensors[0].device} and {t.device}")
+
+
 def _i32(name, t, shape=None):
     if t.dtype != torch.int32 or not t.is_contiguous() or (shape is not None
                                                            and tuple(t.shape) != shape):
@@ -366,6 +374,7 @@ class PagePool:
         for r in (ring_state, out):
             if r.dtype != torch.int64 or r.numel() != 2 or not r.is_contiguous():
                 raise ValueError("ring_state: two int64 values")
+        _one_device(table, free_ring, ring_state, out)
         self.table, self.page_rows, self.free_ring = table, page_rows, free_ring
         self.ring_state, self.ring_state_out = ring_state, out
         self.B = table.shape[0]
@@ -399,6 +408,8 @@ class StepPlan:
                            ("latent_slots", latent_slots, m), ("window_slots", window_slots, m)):
             _i32(name, t, (n,))
             setattr(self, name, t)
+        _one_device(n_tokens, n_latents, swa_len, cu_new, token_seq, positions, latent_slots,
+                    window_slots)
         self.B, self.max_new, self.shape = B, m, n_tokens.shape
         self.c = _StepPlan(n_tokens.data_ptr(), n_latents.data_ptr(), swa_len.data_ptr(),
                            cu_new.data_ptr(), token_seq.data_ptr(), positions.data_ptr(),
@@ -428,6 +439,10 @@ def plan_step(cfg, n_tokens, n_new, pool: PagePool, plan: StepPlan, ws, stream=N
             not (n_tokens.is_contiguous() and n_new.is_contiguous()):
         raise ValueError(f"n_tokens and n_new: contiguous int32 tensors of the plan's {B} requests, "
                          f"the pool's table a row for each")
+    dev = n_tokens.get_device()
+    if n_new.get_device() != dev or pool.table.get_device() != dev or \
+            plan.n_tokens.get_device() != dev or ws.get_device() != dev:
+        _one_device(n_tokens, n_new, pool.table, plan.n_tokens, ws)
     code = load().dsa_plan_step(ctypes.byref(cfg), B, n_tokens.data_ptr(), n_new.data_ptr(),
                                 pool._ref, plan._ref, ws.data_ptr(), ws.numel(),
                                 _launch_stream(n_tokens, stream))
@@ -506,6 +521,7 @@ def norm_rope(positions, heads: HeadSet, rope: Optional[Rope] = None, n_valid=No
             raise ValueError(f"positions: contiguous int32 [{n}]")
     if n_valid is not None:
         _i32("n_valid", n_valid, (1,))
+    _one_device(heads.x, positions, n_valid, None if rope is None else rope.inv_freq)
     code = load().dsa_norm_rope(n, None if n_valid is None else n_valid.data_ptr(),
                                 None if positions is None else positions.data_ptr(), heads.dtype,
                                 heads._c, heads.count, None if rope is None else rope._ref,
@@ -517,7 +533,7 @@ def norm_rope(positions, heads: HeadSet, rope: Optional[Rope] = None, n_valid=No
 _KV_ROW = {KV_BF16: 1024, KV_FP8_E4M3: 512, KV_MXFP4: KV_MXFP4_ROW}
 
 
-def _rows_call(cfg, rows, slots, cache, n_valid):
+def _rows_call(cfg, rows, slots, cache, n_valid, ws):
     """Checks what kv_write and kv_read share; returns (n, row stride, cache rows)."""
     row = _KV_ROW.get(cfg.kv_fmt)
     if row is None:
@@ -533,6 +549,10 @@ def _rows_call(cfg, rows, slots, cache, n_valid):
     width = cache.element_size()
     if not cache.is_contiguous() or cache.shape[-1] * width != row:
         raise ValueError(f"cache: contiguous rows of {row} bytes")
+    dev = rows.get_device()
+    if slots.get_device() != dev or cache.get_device() != dev or ws.get_device() != dev or \
+            (n_valid is not None and n_valid.get_device() != dev):
+        _one_device(rows, slots, cache, ws, n_valid)
     return n, stride[0], cache.numel() * width // row
 
 
@@ -540,7 +560,7 @@ def kv_write(cfg, rows, slots, cache, ws, n_valid=None, stream=None):
     """bf16 rows [n, 512] into a cache of cfg.kv_fmt (dsa_kv_write): row r becomes cache
     row slots[r], negative slots skip; cache: [..., row] contiguous (a pool of pages, or
     the window rows)."""
-    n, stride, n_rows = _rows_call(cfg, rows, slots, cache, n_valid)
+    n, stride, n_rows = _rows_call(cfg, rows, slots, cache, n_valid, ws)
     code = load().dsa_kv_write(ctypes.byref(cfg), n,
                                None if n_valid is None else n_valid.data_ptr(), rows.data_ptr(),
                                stride, slots.data_ptr(), cache.data_ptr(), n_rows, ws.data_ptr(),
@@ -552,7 +572,7 @@ def kv_write(cfg, rows, slots, cache, ws, n_valid=None, stream=None):
 def kv_read(cfg, cache, slots, rows, ws, n_valid=None, stream=None):
     """Rows slots[r] of a cache back as bf16 rows [n, 512] (dsa_kv_read); rows with a
     negative slot are left as they were."""
-    n, stride, n_rows = _rows_call(cfg, rows, slots, cache, n_valid)
+    n, stride, n_rows = _rows_call(cfg, rows, slots, cache, n_valid, ws)
     code = load().dsa_kv_read(ctypes.byref(cfg), n,
                               None if n_valid is None else n_valid.data_ptr(), cache.data_ptr(),
                               n_rows, slots.data_ptr(), rows.data_ptr(), stride, ws.data_ptr(),

@@ -1056,6 +1056,33 @@ dsa_status_t dsa_plan_step(const dsa_config_t* cfg, int B, const int32_t* n_toke
   return DSA_OK;
 }
 
+}  // extern "C"
+
+namespace {
+
+// Whether two of heads x n spans of dim elements (head stride hs, token stride ts) meet:
+// head i of one token and head i + k of another, j tokens apart, are |k hs - j ts| apart.
+bool heads_overlap(int64_t dim, int heads, int64_t hs, int n, int64_t ts) {
+  if ((heads > 1 && hs < dim) || (n > 1 && ts < dim)) return true;
+  if (heads <= 1 || n <= 1) return false;
+  const int64_t huge = int64_t{1} << 62;
+  // the usual layouts: a token's heads together, or a head's tokens
+  if (hs >= huge / heads || ts >= huge / n) return true;  // (spans no address space holds)
+  if (ts >= (heads - 1) * hs + dim || hs >= (n - 1) * ts + dim) return false;
+  // Of the fewer, each distance against the nearest multiples of the other stride.
+  const int64_t a = heads <= n ? hs : ts, b = heads <= n ? ts : hs;
+  const int64_t na = heads <= n ? heads : n, nb = heads <= n ? n : heads;
+  for (int64_t k = 1; k < na; ++k) {
+    const int64_t j = k * a / b, over = k * a - j * b;
+    if ((j < nb && over < dim) || (j + 1 < nb && b - over < dim)) return true;
+  }
+  return false;
+}
+
+}  // namespace
+
+extern "C" {
+
 dsa_status_t dsa_norm_rope(int n, const int32_t* n_valid, const int32_t* positions,
                            dsa_dtype_t dtype, const dsa_heads_t* groups, int n_groups,
                            const dsa_rope_t* rope, dsa_stream_t stream) {
@@ -1094,26 +1121,22 @@ dsa_status_t dsa_norm_rope(int n, const int32_t* n_valid, const int32_t* positio
     }
     if (h.heads == 0 || n == 0) continue;
     if (h.x == nullptr || h.out == nullptr) return DSA_ERR_INVALID_ARG;
+    // (the stride of a single token or head is not used)
+    const int64_t xt = n > 1 ? h.x_token_stride : 0, xh = h.heads > 1 ? h.x_head_stride : 0;
+    const int64_t ot = n > 1 ? h.out_token_stride : 0, oh = h.heads > 1 ? h.out_head_stride : 0;
     if (!aligned16(h.x) || !aligned16(h.out) || (h.norm && h.weight && !aligned16(h.weight)) ||
-        h.x_token_stride % elems || h.x_head_stride % elems || h.out_token_stride % elems ||
-        h.out_head_stride % elems) {
+        xt % elems || xh % elems || ot % elems || oh % elems) {
       return DSA_ERR_MISALIGNED;
     }
-    // no two heads may be written to one place
-    if ((h.heads > 1 && h.out_head_stride < h.dim) || (n > 1 && h.out_token_stride < h.dim)) {
-      return DSA_ERR_INVALID_ARG;
-    }
-    if (h.x == h.out &&
-        (h.x_token_stride != h.out_token_stride || h.x_head_stride != h.out_head_stride)) {
-      return DSA_ERR_INVALID_ARG;
-    }
+    if (heads_overlap(h.dim, h.heads, oh, n, ot)) return DSA_ERR_INVALID_ARG;
+    if (h.x == h.out && (xt != ot || xh != oh)) return DSA_ERR_INVALID_ARG;
     NormRopeSeg& sg = a.seg[used++];
     sg.x = h.x;
     sg.out = h.out;
-    sg.x_token_stride = h.x_token_stride;
-    sg.x_head_stride = h.x_head_stride;
-    sg.out_token_stride = h.out_token_stride;
-    sg.out_head_stride = h.out_head_stride;
+    sg.x_token_stride = xt;
+    sg.x_head_stride = xh;
+    sg.out_token_stride = ot;
+    sg.out_head_stride = oh;
     sg.weight = h.norm ? h.weight : nullptr;
     sg.heads = h.heads;
     sg.dim = h.dim;
@@ -1154,7 +1177,7 @@ dsa_status_t rows_args(const dsa_config_t* cfg, int n, const int32_t* n_valid, c
       (n > 0 && (rows == nullptr || slots == nullptr || (n_rows > 0 && cache == nullptr)))) {
     return DSA_ERR_INVALID_ARG;
   }
-  if (!aligned16(rows) || !aligned16(cache) || row_stride % 8 != 0 ||
+  if (!aligned16(rows) || !aligned16(cache) || (n > 1 && row_stride % 8 != 0) ||
       (reinterpret_cast<uintptr_t>(slots) & 3u) || (reinterpret_cast<uintptr_t>(n_valid) & 3u)) {
     return DSA_ERR_MISALIGNED;
   }
