@@ -1140,7 +1140,7 @@ dsa_status_t dsa_norm_rope(int n, const int32_t* n_valid, const int32_t* positio
     sg.weight = h.norm ? h.weight : nullptr;
     sg.heads = h.heads;
     sg.dim = h.dim;
-    while ((8 << sg.lanes_log2) < h.dim && sg.lanes_log2 < 5) ++sg.lanes_log2;
+    while ((elems << sg.lanes_log2) < h.dim && sg.lanes_log2 < 5) ++sg.lanes_log2;
     sg.unit_begin = static_cast<int>(units);
     units += (int64_t{h.heads} + (32 >> sg.lanes_log2) - 1) / (32 >> sg.lanes_log2);
     if (units > (1 << 24)) return DSA_ERR_UNSUPPORTED;
@@ -1157,6 +1157,7 @@ dsa_status_t dsa_norm_rope(int n, const int32_t* n_valid, const int32_t* positio
   a.n = n;
   a.n_valid = n_valid;
   a.positions = positions;
+  a.n_seg = used;
   a.units = static_cast<int>(units);
   Range range("dsa.norm_rope");
   const cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -321,6 +321,7 @@ struct NormRopeArgs {
   uint64_t inv_2pi;        // 2^66 / (2 pi) (set by the launch)
   int pairs, interleaved;
   float rope_scale;
+  int n_seg;
   int units;       // warps' worth of heads of a token
   int warp_bytes;  // shared memory of a warp (set by the launch)
   NormRopeSeg seg[DSA_MAX_HEAD_GROUPS];

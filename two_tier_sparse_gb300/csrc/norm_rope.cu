@@ -4,13 +4,21 @@
 // position * inv_freq. x is read once and y written once, so the pass is bound
 // by memory (or, for a few tokens, by one trip through it).
 //
-// A unit of work is one head of more than 128 elements (lane l holds 8-element
-// chunks l, l + 32, ...), or two, four ... smaller ones: a warp's worth. Every warp of the
+// A lane holds 16-byte chunks of a head: l, l + 32, ... of one that fills a warp's row of
+// chunks, so that every access of a warp is contiguous (fp32 heads in chunks of 32 bytes a
+// lane took 261 us where this takes 186: 4096 tokens of 64 x 512). A unit of work is one
+// such head, or two, four ... smaller ones: a warp's worth. Every warp of the
 // grid takes an equal run of consecutive units (heads of a token, then the next
 // token's) and works by itself: it copies the elements of the units ahead into a ring of its
 // own (by cp.async; a lane reads back what it copied, so nothing waits for another lane),
-// keeps its group's weights in registers, and works out the cosines and sines when
-// its token changes. So there are always kAhead units of a warp on their way.
+// and works out the cosines and sines when its token changes. Within a run the units of one
+// group of one token share their constants, and a loop for heads that fill every chunk
+// has no branch for lanes without an element: a call that fits in the L2 is bound by the
+// instructions (333 tokens of 89 heads of 128, f16: 9.1 -> 8.2 us; 4096 of them 67.5 -> 52.0).
+// The weights stay in shared memory for their registers' sake. Two CTAs an SM with two
+// units a warp on their way read and write faster than more of either: 4096 tokens of
+// 64 heads of 512, bf16, 581 MB in 92.9 us (6.25 TB/s), a plain copy of as much by the same
+// warps 97.
 // The angles are reduced to a fraction of a turn in 64-bit integers (see turn_bits): an
 // fp32 product would lose the turn's fraction at far positions, and the fp64 pipe would
 // take longer for them than all the rest of a small call.
@@ -24,8 +32,6 @@ namespace dsa {
 namespace {
 
 constexpr int kWarps = 8;
-
-constexpr int kAhead = 3;  // units on their way
 
 // Two fp32 values in a register pair and their arithmetic (one instruction for both).
 using F2 = unsigned long long;
@@ -50,9 +56,9 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
   return r;
 }
 
-// 8 elements in shared or global memory as four pairs of fp32 values, and back.
+// Two 16-bit elements as fp32 values, and back (rounded to nearest even).
 template <typename T>
-__device__ __forceinline__ F2 pair_of(uint32_t w) {  // two 16-bit elements
+__device__ __forceinline__ F2 pair_of(uint32_t w) {
   if constexpr (std::is_same<T, __half>::value) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
     return f2(f.x, f.y);
@@ -71,26 +77,41 @@ __device__ __forceinline__ uint32_t word_of(F2 v) {
     return *reinterpret_cast<const uint32_t*>(&h);
   }
 }
+// A lane's chunk: 16 bytes of a head, as pairs of fp32 values.
 template <typename T>
-__device__ __forceinline__ void store8(T* p, const F2 (&v)[4]) {
+constexpr int kChunk = 16 / static_cast<int>(sizeof(T));  // elements
+template <typename T>
+__device__ __forceinline__ void unpack(uint4 x, F2 (&v)[kChunk<T> / 2]) {
   if constexpr (sizeof(T) == 4) {
-    const float2 a = un2(v[0]), b = un2(v[1]), c = un2(v[2]), d = un2(v[3]);
-    reinterpret_cast<float4*>(p)[0] = make_float4(a.x, a.y, b.x, b.y);
-    reinterpret_cast<float4*>(p)[1] = make_float4(c.x, c.y, d.x, d.y);
+    v[0] = f2(__uint_as_float(x.x), __uint_as_float(x.y));
+    v[1] = f2(__uint_as_float(x.z), __uint_as_float(x.w));
   } else {
-    *reinterpret_cast<uint4*>(p) = make_uint4(word_of<T>(v[0]), word_of<T>(v[1]), word_of<T>(v[2]),
-                                              word_of<T>(v[3]));
+    v[0] = pair_of<T>(x.x), v[1] = pair_of<T>(x.y);
+    v[2] = pair_of<T>(x.z), v[3] = pair_of<T>(x.w);
   }
 }
-__device__ __forceinline__ void load8(const float* p, F2 (&v)[4]) {
-  const float4 x = reinterpret_cast<const float4*>(p)[0], y = reinterpret_cast<const float4*>(p)[1];
-  v[0] = f2(x.x, x.y), v[1] = f2(x.z, x.w), v[2] = f2(y.x, y.y), v[3] = f2(y.z, y.w);
+template <typename T>
+__device__ __forceinline__ uint4 pack(const F2 (&v)[kChunk<T> / 2]) {
+  if constexpr (sizeof(T) == 4) {
+    const float2 a = un2(v[0]), b = un2(v[1]);
+    return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x),
+                      __float_as_uint(b.y));
+  } else {
+    return make_uint4(word_of<T>(v[0]), word_of<T>(v[1]), word_of<T>(v[2]), word_of<T>(v[3]));
+  }
+}
+__device__ __forceinline__ void st_shared_f2x2(uint32_t at, F2 a, F2 b) {
+  asm volatile("st.shared.v2.b64 [%0], {%1, %2};\n" ::"r"(at), "l"(a), "l"(b) : "memory");
+}
+__device__ __forceinline__ void ld_shared_f2x2(uint32_t at, F2& a, F2& b) {
+  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];\n" : "=l"(a), "=l"(b) : "r"(at));
 }
 
 // f / (2 pi) in units of 2^-64 turns, modulo whole turns, rounded down: the fp64 number
 // f = m 2^(e - 1075) with its 53-bit integer m, times 1 / (2 pi) = inv_2pi 2^-66 (inv_2pi
 // the 64-bit integer), is m inv_2pi 2^(e - 1077) of those units. A position times this,
-// modulo 2^64, is the angle's fraction of a turn to within 2^-33 (positions below 2^31).
+// modulo 2^64, is the angle's fraction of a turn to within 2^-33 (positions below 2^31,
+// frequencies of at most a turn a position).
 __device__ __forceinline__ uint64_t turn_bits(double f, uint64_t inv_2pi) {
   const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(f));
   const int e = static_cast<int>(bits >> 52) & 0x7FF;
@@ -108,25 +129,30 @@ __device__ __forceinline__ uint64_t turn_bits(double f, uint64_t inv_2pi) {
   return static_cast<int64_t>(bits) < 0 ? 0ull - t : t;
 }
 
-// Place of pair k in the table of cosines and sines: one place in nine is left out, so that
-// lanes four or eight pairs apart read different banks.
-__host__ __device__ constexpr int table_at(int k) { return k + (k >> 3); }
-__host__ __device__ constexpr int table_len(int pairs) { return (table_at(pairs) + 1) & ~1; }
+// Shared memory of a warp's cosines and sines: (cos, sin) of each pair, or (halves) the
+// cosines, the sines and the negated sines, which the first of a pair's elements take.
+__host__ __device__ constexpr int table_bytes(int pairs, bool interleaved) {
+  return (interleaved ? 8 : 12) * pairs;
+}
 
-// A place in the run of units: the token, the unit of the token and its group of heads,
-// this lane's head, its chunks of the group's heads (as bits) and its first element there
-// (in x or in out), which moves by `step` from unit to unit of a group.
-template <typename T>
-struct Cursor {
-  int tok, u, seg, head;
-  uint32_t chunks;
-  T* ptr;
-  int64_t step;
-};
+// 16 bytes to shared memory by cp.async, or 16 zeros (n = 0: src is not read).
+__device__ __forceinline__ void cp_async_or_zeros(uint32_t dst, const void* src, uint32_t n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
 
-// NV: 8-element chunks a lane holds (heads of up to 256 NV elements).
+// How a group's heads are rotated.
+enum { kStill = 0, kInterleaved = 1, kHalves = 2 };
+
+// Units on their way. (4096 tokens of 64 heads of 512, bf16: 92.9 us with two, 103.9 with three,
+// 112 with one. Heads of 256: 61.2 with two, 57.2 with three.)
+template <int NV>
+constexpr int kUnitsAhead = NV == 2 ? 2 : 3;
+
+// NV: heads of up to 256 NV elements. (CTAs an SM: at NV = 1 three take 51.6 us where four take
+// 53.4, 4096 tokens of 89 heads of 128; at NV = 4 two spill.)
 template <typename T, int NV>
-__global__ void __launch_bounds__(32 * kWarps, NV == 1 ? 4 : NV == 2 ? 3 : 2)
+__global__ void __launch_bounds__(32 * kWarps, NV == 1 ? 3 : NV == 2 ? 2 : 1)
     norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
   extern __shared__ float4 smem4[];
   griddep_wait();
@@ -150,207 +176,249 @@ __global__ void __launch_bounds__(32 * kWarps, NV == 1 ? 4 : NV == 2 ? 3 : 2)
   const int pairs = a.pairs;
   // This warp's shared memory: the ring, (cos, sin) of each pair at its token, and (halves
   // rotated) the rotated elements of its heads.
-  constexpr int kUnitBytes = 256 * NV * static_cast<int>(sizeof(T));
-  constexpr int kQuads = static_cast<int>(sizeof(T)) / 2;  // 16-byte pieces of a chunk
+  constexpr int kAhead = kUnitsAhead<NV>;
+  constexpr int E = kChunk<T>, NC = 256 * NV / (32 * E);  // a lane's chunks
+  constexpr int kUnitBytes = 512 * NC;
   uint8_t* mem = reinterpret_cast<uint8_t*>(smem4) + warp * a.warp_bytes;
-  float2* table = reinterpret_cast<float2*>(mem + kAhead * kUnitBytes);
-  float* stage = reinterpret_cast<float*>(table + table_len(pairs));
-  const uint32_t ring = smem_u32(mem);
+  const uint32_t weights = smem_u32(mem) + kAhead * kUnitBytes + 16u * lane;
+  float* table = reinterpret_cast<float*>(mem + kAhead * kUnitBytes + 1024 * NV);
+  float* stage = table + table_bytes(pairs, a.interleaved) / 4;
+  const uint32_t ring = smem_u32(mem) + 16u * lane;
 
-  // A cursor's place in its group: the lane's head and pointer.
-  auto enter = [&](Cursor<T>& c, bool in) {
-    const NormRopeSeg& sg = a.seg[c.seg];
-    const int lg = sg.lanes_log2;
-    c.head = ((c.u - sg.unit_begin) << (5 - lg)) + (lane >> lg);
-    const int64_t ts = in ? sg.x_token_stride : sg.out_token_stride;
-    const int64_t hs = in ? sg.x_head_stride : sg.out_head_stride;
-    const int l = lane & ((1 << lg) - 1);
-    c.ptr = static_cast<T*>(in ? const_cast<void*>(sg.x) : sg.out) + c.tok * ts + c.head * hs + 8 * l;
-    c.step = hs << (5 - lg);
-    c.chunks = 0;
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      if (8 * (l + (k << lg)) < sg.dim) c.chunks |= 1u << k;
-    }
-  };
-  auto advance = [&](Cursor<T>& c, bool in) {
-    ++c.u;
-    if (c.u < a.seg[c.seg].unit_end) {
-      c.head += 32 >> a.seg[c.seg].lanes_log2;
-      c.ptr += c.step;
-      return;
-    }
-    if (c.u == a.units) {
-      c.u = 0;
-      c.seg = 0;
-      ++c.tok;
-    } else {
-      ++c.seg;
-    }
-    enter(c, in);
-  };
-  Cursor<T> ahead;
-  ahead.tok = total <= 0x7FFFFFFF ? static_cast<int>(begin) / a.units
-                                  : static_cast<int>(begin / a.units);
-  ahead.u = static_cast<int>(begin - static_cast<int64_t>(ahead.tok) * a.units);
-  ahead.seg = 0;
-  while (ahead.u >= a.seg[ahead.seg].unit_end) ++ahead.seg;
-  Cursor<T> at;
-  at.tok = ahead.tok, at.u = ahead.u, at.seg = ahead.seg;
-  enter(ahead, true);
-  enter(at, false);
-  int issued = 0;
+  // The run's first unit: token, group, unit of the token.
+  int tok = total <= 0x7FFFFFFF ? static_cast<int>(begin) / a.units
+                                : static_cast<int>(begin / a.units);
+  int u = static_cast<int>(begin - static_cast<int64_t>(tok) * a.units);
+  int s = 0;
+  while (u >= a.seg[s].unit_end) ++s;
+
+  // The copies: the next unit's place and what it takes to step on within its group.
+  int in_tok = tok, in_s = s, in_u = u, in_left = count;
+  const T* in;
+  int64_t in_step;
+  int in_end, in_lim, in_chunk;
+  uint32_t in_bytes[NC];
   uint32_t slot = ring;  // of the next unit to copy
-  auto issue = [&]() {   // one copy group a unit, empty past the end
-    if (issued < count) {
-      const NormRopeSeg& sg = a.seg[ahead.seg];
-      const uint32_t m = ahead.head < sg.heads ? ahead.chunks : 0u;
+  auto in_enter = [&]() {
+    const NormRopeSeg& sg = a.seg[in_s];
+    const int lg = sg.lanes_log2, l = lane & ((1 << lg) - 1);
+    const int head = ((in_u - sg.unit_begin) << (5 - lg)) + (lane >> lg);
+    in = static_cast<const T*>(sg.x) + in_tok * sg.x_token_stride + head * sg.x_head_stride + E * l;
+    in_step = sg.x_head_stride << (5 - lg);
+    in_end = sg.unit_end;
+    // the lane has a head in the units below in_lim
+    in_lim = sg.unit_end - ((sg.heads - 1) % (32 >> lg) < (lane >> lg) ? 1 : 0);
+    in_chunk = E << lg;
 #pragma unroll
-      for (int c = 0; c < NV; ++c) {
-        if (m >> c & 1u) {
+    for (int c = 0; c < NC; ++c) in_bytes[c] = E * (l + (c << lg)) < sg.dim ? 16u : 0u;
+  };
+  in_enter();
+  auto issue = [&]() {  // one copy group a unit, empty past the end
+    if (in_left > 0) {
+      const bool mine = in_u < in_lim;
 #pragma unroll
-          for (int k = 0; k < kQuads; ++k) {
-            cp_async_16(slot + ((c * kQuads + k) * 32 + lane) * 16,
-                        reinterpret_cast<const uint4*>(ahead.ptr + (8 * c << sg.lanes_log2)) + k);
-          }
-        }
+      for (int c = 0; c < NC; ++c) {
+        cp_async_or_zeros(slot + c * 512, in + c * in_chunk, mine ? in_bytes[c] : 0u);
       }
-      advance(ahead, true);
+      in += in_step;
+      --in_left;
+      if (++in_u == in_end) {
+        if (++in_s == a.n_seg) {
+          in_s = in_u = 0;
+          ++in_tok;
+        }
+        in_enter();
+      }
     }
-    ++issued;
     slot = slot == ring + (kAhead - 1) * kUnitBytes ? ring : slot + kUnitBytes;
     cp_async_commit();
   };
 #pragma unroll 1
   for (int i = 0; i < kAhead; ++i) issue();
-  F2 w[NV][4];  // the group's weights
-  int weights_of = -1, table_of = -1;
-#pragma unroll 1
-  for (int i = 0; i < count; ++i) {
-    const NormRopeSeg& sg = a.seg[at.seg];
-    const int lg = sg.lanes_log2, l = lane & ((1 << lg) - 1);
-    if (weights_of != at.seg) {
-      weights_of = at.seg;
+
+  int table_of = -1, weights_of = -1, left = count;
+  do {
+    // The run's units of one group of one token.
+    const NormRopeSeg& sg = a.seg[s];
+    const int lg = sg.lanes_log2, l = lane & ((1 << lg) - 1), chunk = E << lg;
+    const int units = min(left, sg.unit_end - u);
+    const int head = ((u - sg.unit_begin) << (5 - lg)) + (lane >> lg);
+    const int mine = ((sg.heads - 1 - head) >> (5 - lg)) + 1;  // of them, those with a head for the lane
+    T* out = static_cast<T*>(sg.out) + tok * sg.out_token_stride + head * sg.out_head_stride + E * l;
+    const int64_t out_step = sg.out_head_stride << (5 - lg);
+    const float inv_dim = sg.inv_dim, eps = sg.eps;
+    const bool norm = sg.norm != 0;
+    const int dim = sg.dim, K = (dim + chunk - 1) >> (lg + (E == 8 ? 3 : 2));
+    if (weights_of != s) {  // the group's weights: each lane its own elements'
+      weights_of = s;
 #pragma unroll
-      for (int c = 0; c < NV; ++c) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) w[c][k] = f2(1.f, 1.f);
-        if (sg.weight && (at.chunks >> c & 1u)) load8(sg.weight + 8 * (l + (c << lg)), w[c]);
+      for (int q = 0; q < NC * E / 4; ++q) {
+        const int e = E * l + (4 * q / E) * chunk + 4 * q % E;
+        float4 w = make_float4(1.f, 1.f, 1.f, 1.f);
+        if (sg.weight && e < dim) w = *reinterpret_cast<const float4*>(sg.weight + e);
+        st_shared_f2x2(weights + q * 512, f2(w.x, w.y), f2(w.z, w.w));
       }
     }
-    if (sg.rope && table_of != at.tok) {
-      table_of = at.tok;
-      const int64_t pos = a.positions[at.tok];
+    if (sg.rope && table_of != tok) {
+      table_of = tok;
+      const int64_t pos = a.positions[tok];
       __syncwarp();
       for (int k = lane; k < pairs; k += 32) {
         const int64_t turn = pos * static_cast<int64_t>(turn_bits(a.inv_freq[k], a.inv_2pi));
-        float s, c;
-        sincospif(static_cast<float>(turn) * 0x1p-63f, &s, &c);  // half turns, from -1 to 1
-        table[table_at(k)] = make_float2(c * a.rope_scale, s * a.rope_scale);
+        float sn, cs;
+        sincospif(static_cast<float>(turn) * 0x1p-63f, &sn, &cs);  // half turns, from -1 to 1
+        cs *= a.rope_scale;
+        sn *= a.rope_scale;
+        if (a.interleaved) {
+          reinterpret_cast<float2*>(table)[k] = make_float2(cs, sn);
+        } else {
+          table[k] = cs;
+          table[pairs + k] = sn;
+          table[2 * pairs + k] = -sn;
+        }
       }
       __syncwarp();
     }
-    cp_async_wait<kAhead - 1>();
-    const uint32_t m = at.head < sg.heads ? at.chunks : 0u;
-    F2 v[NV][4];
-    F2 ss0 = f2(0.f, 0.f), ss1 = ss0;
+    const int start = sg.rope_start;
+    // The units. `full`: heads of 256 NV elements, one a warp, so every lane has every chunk.
+    auto run = [&](auto full_c, auto rope_c) {
+      constexpr bool kFull = decltype(full_c)::value;
+      constexpr int kRope = decltype(rope_c)::value;
+      T* to = out;
+#pragma unroll 1
+      for (int i = 0; i < units; ++i) {
+        cp_async_wait<kAhead - 1>();
+        F2 v[NC][E / 2];
+        F2 ss0 = f2(0.f, 0.f), ss1 = ss0;
 #pragma unroll
-    for (int c = 0; c < NV; ++c) {
-      // `slot` is the place of this unit, refilled below
-      if (m >> c & 1u) {
-        const uint4 x = ld_shared_v4(slot + (c * kQuads * 32 + lane) * 16);
-        if constexpr (sizeof(T) == 4) {
-          const uint4 y = ld_shared_v4(slot + ((c * kQuads + 1) * 32 + lane) * 16);
-          v[c][0] = f2(__uint_as_float(x.x), __uint_as_float(x.y));
-          v[c][1] = f2(__uint_as_float(x.z), __uint_as_float(x.w));
-          v[c][2] = f2(__uint_as_float(y.x), __uint_as_float(y.y));
-          v[c][3] = f2(__uint_as_float(y.z), __uint_as_float(y.w));
+        for (int c = 0; c < NC; ++c) {
+          if (kFull || c == 0 || c < K) {
+            unpack<T>(ld_shared_v4(slot + c * 512), v[c]);  // (the place refilled below)
+#pragma unroll
+            for (int k = 0; k < E / 2; k += 2) {
+              ss0 = fma2(v[c][k], v[c][k], ss0);
+              ss1 = fma2(v[c][k + 1], v[c][k + 1], ss1);
+            }
+          }
+        }
+        issue();
+        const float2 s0 = un2(ss0), s1 = un2(ss1);
+        float ss = (s0.x + s0.y) + (s1.x + s1.y);
+        if constexpr (kFull) {
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
         } else {
-          v[c][0] = pair_of<T>(x.x), v[c][1] = pair_of<T>(x.y);
-          v[c][2] = pair_of<T>(x.z), v[c][3] = pair_of<T>(x.w);
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+            const float t = __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+            if (o < 1 << lg) ss += t;
+          }
         }
-        ss0 = fma2(v[c][0], v[c][0], ss0);
-        ss1 = fma2(v[c][1], v[c][1], ss1);
-        ss0 = fma2(v[c][2], v[c][2], ss0);
-        ss1 = fma2(v[c][3], v[c][3], ss1);
-      }
-    }
-    issue();
-    if (sg.norm) {
-      const float2 s0 = un2(ss0), s1 = un2(ss1);
-      float ss = (s0.x + s0.y) + (s1.x + s1.y);
-      for (int o = (1 << lg) >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-      const float r = rsqrtf(ss * sg.inv_dim + sg.eps);
-      const F2 r2 = f2(r, r);
+        const float r = norm ? rsqrtf(fmaf(ss, inv_dim, eps)) : 1.f;
+        const F2 r2 = f2(r, r);
 #pragma unroll
-      for (int c = 0; c < NV; ++c) {
+        for (int c = 0; c < NC; ++c) {
+          if (kFull || c == 0 || c < K) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[c][k] = mul2(v[c][k], mul2(r2, w[c][k]));
-      }
-    }
-    if (sg.rope) {
-      const int rd = 2 * pairs;
-      if (a.interleaved) {
-#pragma unroll
-        for (int c = 0; c < NV; ++c) {
-          const int e = 8 * (l + (c << lg)) - sg.rope_start;
-          if (e >= 0 && e < rd) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 t = table[table_at((e >> 1) + k)], x = un2(v[c][k]);
-              v[c][k] = f2(x.x * t.x - x.y * t.y, x.x * t.y + x.y * t.x);
+            for (int k = 0; k < E / 2; k += 2) {
+              F2 w0, w1;
+              ld_shared_f2x2(weights + (c * E + 2 * k) / 4 * 512, w0, w1);
+              v[c][k] = mul2(v[c][k], mul2(r2, w0));
+              v[c][k + 1] = mul2(v[c][k + 1], mul2(r2, w1));
             }
           }
         }
-      } else {
-        // element i and element i + rope_dim / 2 turn together: through shared memory, the
-        // first and the last four elements of the chunks apart (16 bytes from lane to lane)
-        float4* heads = reinterpret_cast<float4*>(stage + (lane >> lg) * rd);
-        const int last4 = rd >> 3;
+        if constexpr (kRope == kInterleaved) {
 #pragma unroll
-        for (int c = 0; c < NV; ++c) {
-          const int e = 8 * (l + (c << lg)) - sg.rope_start;
-          if (e >= 0 && e < rd) {
-            const float2 x0 = un2(v[c][0]), x1 = un2(v[c][1]), x2 = un2(v[c][2]), x3 = un2(v[c][3]);
-            heads[e >> 3] = make_float4(x0.x, x0.y, x1.x, x1.y);
-            heads[last4 + (e >> 3)] = make_float4(x2.x, x2.y, x3.x, x3.y);
+          for (int c = 0; c < NC; ++c) {
+            const int e = E * l + c * chunk - start;
+            if (static_cast<unsigned>(e) < static_cast<unsigned>(2 * pairs)) {
+#pragma unroll
+              for (int k = 0; k < E / 2; k += 2) {  // two pairs: cosine, sine, cosine, sine
+                const float4 t = *reinterpret_cast<const float4*>(table + e + 2 * k);
+                const float2 x = un2(v[c][k]), y = un2(v[c][k + 1]);
+                v[c][k] = f2(x.x * t.x - x.y * t.y, x.x * t.y + x.y * t.x);
+                v[c][k + 1] = f2(y.x * t.z - y.y * t.w, y.x * t.w + y.y * t.z);
+              }
+            }
           }
+        } else if constexpr (kRope == kHalves) {
+          // element i and element i + rope_dim / 2 turn together: through shared memory, the
+          // chunks' quarters of four elements apart (16 bytes from lane to lane)
+          const int rd = 2 * pairs;
+          float4* heads = reinterpret_cast<float4*>(stage + (lane >> lg) * rd);
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const int e = E * l + c * chunk - start;
+            if (static_cast<unsigned>(e) < static_cast<unsigned>(rd)) {
+#pragma unroll
+              for (int k = 0; k < E / 2; k += 2) {
+                const float2 x = un2(v[c][k]), y = un2(v[c][k + 1]);
+                heads[static_cast<unsigned>(e + k / 2 * rd) / E] = make_float4(x.x, x.y, y.x, y.y);
+              }
+            }
+          }
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const int e = E * l + c * chunk - start;
+            if (static_cast<unsigned>(e) < static_cast<unsigned>(rd)) {
+              const bool low = e < pairs;
+              const int there = low ? e + pairs : e - pairs;
+              const float* cs = table + (low ? e : there);
+              const float* sn = cs + (low ? rd : pairs);  // the low one's sine is negated
+#pragma unroll
+              for (int k = 0; k < E / 2; k += 2) {
+                const float4 y = heads[static_cast<unsigned>(there + k / 2 * rd) / E];
+                const float4 p = *reinterpret_cast<const float4*>(cs + 2 * k);
+                const float4 q = *reinterpret_cast<const float4*>(sn + 2 * k);
+                v[c][k] = fma2(f2(y.x, y.y), f2(q.x, q.y), mul2(v[c][k], f2(p.x, p.y)));
+                v[c][k + 1] = fma2(f2(y.z, y.w), f2(q.z, q.w), mul2(v[c][k + 1], f2(p.z, p.w)));
+              }
+            }
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        if (kFull || i < mine) {
 #pragma unroll
-        for (int c = 0; c < NV; ++c) {
-          const int e = 8 * (l + (c << lg)) - sg.rope_start;
-          if (e >= 0 && e < rd) {
-            const bool low = e < pairs;
-            const int there = (low ? e + pairs : e - pairs) >> 3;
-            const float4 o0 = heads[there], o1 = heads[last4 + there];
-            const float2 other[4] = {{o0.x, o0.y}, {o0.z, o0.w}, {o1.x, o1.y}, {o1.z, o1.w}};
-            const int p0 = low ? e : e - pairs;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 t0 = table[table_at(p0 + 2 * k)], t1 = table[table_at(p0 + 2 * k + 1)];
-              const float2 x = un2(v[c][k]), y = other[k];
-              v[c][k] = low ? f2(x.x * t0.x - y.x * t0.y, x.y * t1.x - y.y * t1.y)
-                            : f2(y.x * t0.y + x.x * t0.x, y.y * t1.y + x.y * t1.x);
+          for (int c = 0; c < NC; ++c) {
+            if (kFull || E * l + c * chunk < dim) {
+              *reinterpret_cast<uint4*>(to + c * chunk) = pack<T>(v[c]);
             }
           }
         }
-        __syncwarp();
+        to += out_step;
       }
+    };
+    using std::integral_constant;
+    const bool full = dim == 256 * NV;
+    const int rope = !sg.rope ? kStill : a.interleaved ? kInterleaved : kHalves;
+    if (full && rope == kInterleaved) {
+      run(std::true_type{}, integral_constant<int, kInterleaved>{});
+    } else if (full && rope == kStill) {
+      run(std::true_type{}, integral_constant<int, kStill>{});
+    } else if (rope == kInterleaved) {
+      run(std::false_type{}, integral_constant<int, kInterleaved>{});
+    } else if (rope == kStill) {
+      run(std::false_type{}, integral_constant<int, kStill>{});
+    } else {
+      run(std::false_type{}, integral_constant<int, kHalves>{});
     }
-#pragma unroll
-    for (int c = 0; c < NV; ++c) {
-      if (m >> c & 1u) store8(at.ptr + (8 * c << lg), v[c]);
+    left -= units;
+    u += units;
+    if (++s == a.n_seg) {
+      s = u = 0;
+      ++tok;
     }
-    advance(at, false);
-  }
+  } while (left > 0);
 }
 
 template <typename T, int NV>
 cudaError_t launch_nv(NormRopeArgs a, cudaStream_t s) {
   const int stage = a.pairs && !a.interleaved ? 256 * NV * 4 : 0;
   a.inv_2pi = static_cast<uint64_t>(0x1p66L * 0.15915494309189533576888376337251436203445965L);
-  a.warp_bytes = kAhead * 256 * NV * static_cast<int>(sizeof(T)) + table_len(a.pairs) * 8 + stage;
+  a.warp_bytes = kUnitsAhead<NV> * 256 * NV * static_cast<int>(sizeof(T)) + 1024 * NV +
+                 table_bytes(a.pairs, a.interleaved) + stage;
   const int smem = kWarps * a.warp_bytes;
   static std::atomic<int> smem_set[64]{};
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(norm_rope_kernel<T, NV>), smem, smem_set);
