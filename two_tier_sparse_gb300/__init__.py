@@ -533,52 +533,54 @@ def norm_rope(positions, heads: HeadSet, rope: Optional[Rope] = None, n_valid=No
 _KV_ROW = {KV_BF16: 1024, KV_FP8_E4M3: 512, KV_MXFP4: KV_MXFP4_ROW}
 
 
-def _rows_call(cfg, rows, slots, cache, n_valid, ws):
-    """Checks what kv_write and kv_read share; returns (n, row stride, cache rows)."""
+def _rows_call(name, cfg, rows, slots, cache, ws, n_valid, stream):
+    """kv_write and kv_read: their checks and the call."""
     row = _KV_ROW.get(cfg.kv_fmt)
     if row is None:
         raise DsaError(1, "kv_fmt")
-    shape, stride = rows.shape, rows.stride()
-    if _DT.get(rows.dtype) != 0 or len(shape) != 2 or shape[1] != 512 or stride[1] != 1:
+    shape = rows.shape
+    if len(shape) != 2 or shape[1] != 512 or _DT.get(rows.dtype) != 0:
         raise ValueError("rows: bf16 (or its bits in int16) [n, 512] with contiguous elements")
-    n = shape[0]
-    if slots.dtype is not torch.int32 or slots.shape != shape[:1] or not slots.is_contiguous():
+    n, stride = shape[0], 512
+    if not rows.is_contiguous():
+        stride, unit = rows.stride()
+        if unit != 1:
+            raise ValueError("rows: contiguous elements")
+    if slots.dtype is not torch.int32 or slots.numel() != n or slots.dim() != 1 or \
+            not slots.is_contiguous():
         _i32("slots", slots, (n,))
     if n_valid is not None:
         _i32("n_valid", n_valid, (1,))
-    width = cache.element_size()
-    if not cache.is_contiguous() or cache.shape[-1] * width != row:
+    if not cache.is_contiguous() or cache.shape[-1] * cache.element_size() != row:
         raise ValueError(f"cache: contiguous rows of {row} bytes")
     dev = rows.get_device()
     if slots.get_device() != dev or cache.get_device() != dev or ws.get_device() != dev or \
             (n_valid is not None and n_valid.get_device() != dev):
         _one_device(rows, slots, cache, ws, n_valid)
-    return n, stride[0], cache.numel() * width // row
+    s = _launch_stream(rows, stream)
+    valid = None if n_valid is None else n_valid.data_ptr()
+    n_rows, c = cache.nbytes // row, ctypes.byref(cfg)
+    if name == "dsa_kv_write":
+        code = load().dsa_kv_write(c, n, valid, rows.data_ptr(), stride, slots.data_ptr(),
+                                   cache.data_ptr(), n_rows, ws.data_ptr(), ws.numel(), s)
+    else:
+        code = load().dsa_kv_read(c, n, valid, cache.data_ptr(), n_rows, slots.data_ptr(),
+                                  rows.data_ptr(), stride, ws.data_ptr(), ws.numel(), s)
+    if code:
+        raise DsaError(code, name)
 
 
 def kv_write(cfg, rows, slots, cache, ws, n_valid=None, stream=None):
     """bf16 rows [n, 512] into a cache of cfg.kv_fmt (dsa_kv_write): row r becomes cache
     row slots[r], negative slots skip; cache: [..., row] contiguous (a pool of pages, or
     the window rows)."""
-    n, stride, n_rows = _rows_call(cfg, rows, slots, cache, n_valid, ws)
-    code = load().dsa_kv_write(ctypes.byref(cfg), n,
-                               None if n_valid is None else n_valid.data_ptr(), rows.data_ptr(),
-                               stride, slots.data_ptr(), cache.data_ptr(), n_rows, ws.data_ptr(),
-                               ws.numel(), _launch_stream(rows, stream))
-    if code:
-        raise DsaError(code, "dsa_kv_write")
+    _rows_call("dsa_kv_write", cfg, rows, slots, cache, ws, n_valid, stream)
 
 
 def kv_read(cfg, cache, slots, rows, ws, n_valid=None, stream=None):
     """Rows slots[r] of a cache back as bf16 rows [n, 512] (dsa_kv_read); rows with a
     negative slot are left as they were."""
-    n, stride, n_rows = _rows_call(cfg, rows, slots, cache, n_valid, ws)
-    code = load().dsa_kv_read(ctypes.byref(cfg), n,
-                              None if n_valid is None else n_valid.data_ptr(), cache.data_ptr(),
-                              n_rows, slots.data_ptr(), rows.data_ptr(), stride, ws.data_ptr(),
-                              ws.numel(), _launch_stream(rows, stream))
-    if code:
-        raise DsaError(code, "dsa_kv_read")
+    _rows_call("dsa_kv_read", cfg, rows, slots, cache, ws, n_valid, stream)
 
 
 def read_device_status(ws, stream=None):
