@@ -190,6 +190,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     n_vis = a.n_latents[b];
     n_sw = a.swa_len[b];
   }
+  // A math thread's token ids, read once the previous kernel's are final.
+  constexpr int kPer = kMaxKTokens / 128;  // 4
+  int my[kPer];
+  auto read_ids = [&]() {
+    const int32_t* tk = a.token_ids + static_cast<int64_t>(b) * a.k_tokens;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = tid * kPer + j;
+      my[j] = i < a.k_tokens ? tk[i] : -1;
+    }
+  };
 
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
@@ -221,6 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     griddep_wait();
     n_vis = a.n_latents[b];
     n_sw = a.swa_len[b];
+    if (tid < 128) read_ids();
   }
   if (n_sw < 0 || n_sw > a.window) {
     if (tid == 0 && split == 0) report(a.status, static_cast<uint32_t>(b));
@@ -258,26 +270,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Compact the valid token ids (>= 0 and < n_vis) in order (math threads,
   // once the previous kernel's ids are final).
   if (tid < 128) {
-    griddep_wait();
-    const int32_t* tk = a.token_ids + static_cast<int64_t>(b) * a.k_tokens;
-    constexpr int kPer = kMaxKTokens / 128;  // 4
-    int my[kPer];
+    if (!a.wait_first) {
+      griddep_wait();
+      read_ids();
+    }
     int cnt = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const int i = tid * kPer + j;
-      int id = -1;
-      if (i < a.k_tokens) {
-        id = tk[i];
-        if (id >= n_vis) {
-          if (split == 0) report(a.status, static_cast<uint32_t>(id));
-          id = -1;
-        }
-        if (paged && id >= 0) {
-          const int64_t row = paged_row(a.pages, b, id);
-          if (row < 0 && split == 0) report(a.status, static_cast<uint32_t>(id));
-          id = static_cast<int>(row);
-        }
+      int id = my[j];
+      if (id >= n_vis) {
+        if (split == 0) report(a.status, static_cast<uint32_t>(id));
+        id = -1;
+      }
+      if (paged && id >= 0) {
+        const int64_t row = paged_row(a.pages, b, id);
+        if (row < 0 && split == 0) report(a.status, static_cast<uint32_t>(id));
+        id = static_cast<int>(row);
       }
       my[j] = id;
       cnt += id >= 0 ? 1 : 0;
@@ -374,13 +382,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const uint32_t slot = static_cast<uint32_t>(sl * kSlotBytes);
         const uint32_t sw[4] = {scales.x, scales.y, scales.z, scales.w};
+        // (a warp past the last step of 16 rows has nothing that PV reads)
+        if (8 * (w & ~1) < n_rows_cta - done * kRows) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {  // piece g + 4 i: its scale is byte g of word i
-          const uint32_t f = mx4_scale_bf16x2((sw[i] >> (8u * g)) & 0xFFu);
-          const uint32_t cw[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+          for (int i = 0; i < 4; ++i) {  // piece g + 4 i: its scale is byte g of word i
+            const uint32_t f = mx4_scale_bf16x2((sw[i] >> (8u * g)) & 0xFFu);
+            const uint32_t cw[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            st_shared_v4(to[n] + slot + 2 * i * kAtomBytes, mx4_decode8(cw[n], f));
+            for (int n = 0; n < 4; ++n) {
+              st_shared_v4(to[n] + slot + 2 * i * kAtomBytes, mx4_decode8(cw[n], f));
+            }
           }
         }
         fence_proxy_async_smem();  // the MMAs read the tile through the async proxy
@@ -404,12 +415,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     n_tiles_e = have_ids ? n_tiles : 0;
   } else if (warp == kMmaWarp || warp == kPvWarp) {
     // ---------------- MMA issuers ----------------
-    int n_tiles = 0;
+    int n_rows_cta = 0;
     if (wait_bar(&misc->ids_ready, 0u, misc, a.status)) {
       int s_begin, s_cnt;
       sel_range(misc->n_sel, s_begin, s_cnt);
-      n_tiles = (w_cnt + s_cnt + kRows - 1) / kRows;
+      n_rows_cta = w_cnt + s_cnt;
     }
+    const int n_tiles = (n_rows_cta + kRows - 1) / kRows;
     // PV(t) is issued only after the softmax of tile t, hence after QK^T(t)
     // completed: its commit alone frees the tile's slot, and the PV issuer's
     // last commit means every MMA of the CTA has completed.
@@ -428,6 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         fence_proxy_async_smem();
         uint32_t a_lo = lo(kv_mn) + static_cast<uint32_t>(sl * kSlotBytes >> 4);
+        const int steps = (n_rows_cta - t * kRows + 15) >> 4;  // of 16 rows: those with any
 #pragma unroll 1
         for (int m = 0; m < 4; ++m) {
 #pragma unroll
@@ -435,6 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_warp<false>(leader, tmem + kTmemO + 64 * m, a_lo + ((ks * 16 * 128) >> 4), hi(kv_mn),
                             lo(p_k) + ((ks * 32) >> 4), hi(p_k), idesc_o,
                             (t > 0 || ks > 0) ? 1u : 0u);
+            if (ks + 1 >= steps) break;
           }
           a_lo += (2 * kAtomBytes) >> 4;
         }
