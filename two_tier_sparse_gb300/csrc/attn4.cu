@@ -336,18 +336,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       to[n] = sbase + kKV + (g >> 1) * kAtomBytes + (8u * w + r) * 128u +
               (((4u * (g & 1u) + n) ^ r) << 4);
     }
-    uint4 code[4], scales;
     int next = 0, done = 0;  // tiles read, tiles converted
-    for (;;) {
-      const bool conv = next > done;
-      // The next tile is read in this pass, unless that needs ids that are not there
-      // yet while a tile is at hand (the conversion then goes first).
-      bool read = !have_ids && (next + 1) * kRows <= w_cnt;
-      if (!have_ids && !read &&
-          (!conv || __all_sync(0xFFFFFFFFu, mbar_try_wait(smem_u32(&misc->ids_ready), 0u)))) {
+    // Reads the next tile into (code, scales): 1; 0 if it needs ids that are not there yet (and
+    // `block` is not set); -1 if there is none, or the wait for the ids ran out (ok is false).
+    auto read = [&](uint4 (&code)[4], uint4& scales, bool block) -> int {
+      if (!have_ids && (next + 1) * kRows > w_cnt) {
+        if (!block && !__all_sync(0xFFFFFFFFu, mbar_try_wait(smem_u32(&misc->ids_ready), 0u))) return 0;
         if (!wait_bar(&misc->ids_ready, 0u, misc, a.status)) {
           ok = false;
-          break;
+          return -1;
         }
         int s_cnt;
         sel_range(misc->n_sel, s_begin, s_cnt);
@@ -355,11 +352,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         n_tiles = (n_rows_cta + kRows - 1) / kRows;
         have_ids = true;
       }
-      if (have_ids) read = next < n_tiles;
-      if (!conv && !read) break;
-      const uint8_t* src = nullptr;  // this lane's row of the next tile
+      if (have_ids && next >= n_tiles) return -1;
+      const uint8_t* src = nullptr;  // this lane's row of the tile
       const int row_g = next * kRows + 8 * w + static_cast<int>(r);
-      if (read && row_g < n_rows_cta) {
+      if (row_g < n_rows_cta) {
         if (row_g < w_cnt) {
           const int64_t row = wrow0 + w_begin + row_g;
           if (DSA_DCHECK(row >= 0 && row < a.swa_rows, a.status, SITE_ATTN, row)) {
@@ -372,45 +368,57 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (conv) {
-        const int sl = done % kSlots;
-        if (done >= kSlots &&
-            !wait_bar(&misc->kv_empty[sl], static_cast<uint32_t>(((done / kSlots) - 1) & 1), misc,
-                      a.status)) {
-          ok = false;
-          break;
-        }
-        const uint32_t slot = static_cast<uint32_t>(sl * kSlotBytes);
-        const uint32_t sw[4] = {scales.x, scales.y, scales.z, scales.w};
-        // (a warp past the last step of 16 rows has nothing that PV reads)
-        if (8 * (w & ~1) < n_rows_cta - done * kRows) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {  // piece g + 4 i: its scale is byte g of word i
-            const uint32_t f = mx4_scale_bf16x2((sw[i] >> (8u * g)) & 0xFFu);
-            const uint32_t cw[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+      for (int i = 0; i < 4; ++i) code[i] = make_uint4(0u, 0u, 0u, 0u);
+      scales = make_uint4(0u, 0u, 0u, 0u);
+      if (src != nullptr) {
+        const uint4* p = reinterpret_cast<const uint4*>(src);
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              st_shared_v4(to[n] + slot + 2 * i * kAtomBytes, mx4_decode8(cw[n], f));
-            }
+        for (int i = 0; i < 4; ++i) code[i] = __ldg(p + g + 4 * i);
+        scales = __ldg(p + kRow4Codes / 16);
+      }
+      ++next;
+      return 1;
+    };
+    // Converts tile `done` into its slot.
+    auto convert = [&](const uint4 (&code)[4], const uint4& scales) {
+      const int sl = done % kSlots;
+      if (done >= kSlots && !wait_bar(&misc->kv_empty[sl],
+                                      static_cast<uint32_t>(((done / kSlots) - 1) & 1), misc,
+                                      a.status)) {
+        ok = false;
+        return;
+      }
+      const uint32_t slot = static_cast<uint32_t>(sl * kSlotBytes);
+      const uint32_t sw[4] = {scales.x, scales.y, scales.z, scales.w};
+      // (a warp past the last step of 16 rows has nothing that PV reads)
+      if (8 * (w & ~1) < n_rows_cta - done * kRows) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // piece g + 4 i: its scale is byte g of word i
+          const uint32_t f = mx4_scale_bf16x2((sw[i] >> (8u * g)) & 0xFFu);
+          const uint32_t cw[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            st_shared_v4(to[n] + slot + 2 * i * kAtomBytes, mx4_decode8(cw[n], f));
           }
         }
-        fence_proxy_async_smem();  // the MMAs read the tile through the async proxy
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&misc->kv_full[sl]);
-        ++done;
       }
-      if (read) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) code[i] = make_uint4(0u, 0u, 0u, 0u);
-        scales = make_uint4(0u, 0u, 0u, 0u);
-        if (src != nullptr) {
-          const uint4* p = reinterpret_cast<const uint4*>(src);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) code[i] = __ldg(p + g + 4 * i);
-          scales = __ldg(p + kRow4Codes / 16);
-        }
-        ++next;
-      }
+      fence_proxy_async_smem();  // the MMAs read the tile through the async proxy
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&misc->kv_full[sl]);
+      ++done;
+    };
+    // One pass: the next tile is read into one set of registers (x) while the one before it
+    // is converted from the other (y).
+    auto pass = [&](uint4 (&x)[4], uint4& xs, const uint4 (&y)[4], const uint4& ys) -> bool {
+      const bool at_hand = next > done;
+      int got = read(x, xs, !at_hand);
+      if (ok && at_hand) convert(y, ys);
+      if (ok && got == 0) got = read(x, xs, true);
+      return ok && got > 0;
+    };
+    uint4 code0[4], code1[4], scales0, scales1;
+    while (pass(code0, scales0, code1, scales1) && pass(code1, scales1, code0, scales0)) {
     }
     n_tiles_e = have_ids ? n_tiles : 0;
   } else if (warp == kMmaWarp || warp == kPvWarp) {
