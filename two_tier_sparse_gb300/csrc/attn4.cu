@@ -79,7 +79,7 @@ static_assert(2 * xchg_bytes(2) <= kKVBytes && 4 * xchg_bytes(4) <= kKVBytes &&
               "receive areas fit the slots");
 
 struct Misc {
-  uint64_t kv_full[kSlots], kv_empty[kSlots], s_full[2], s_free[2], p_full, p_empty;
+  uint64_t kv_full[kSlots][2], kv_empty[kSlots][2], s_full[2], s_free[2], p_full, p_empty;
   uint64_t q_done, ids_ready;
   uint64_t o_done;  // every MMA of the CTA has completed
   uint32_t tmem_base;
@@ -172,6 +172,11 @@ __device__ __forceinline__ void stage_heads(uint32_t image, uint32_t row, int h0
   }
 }
 
+// kParts: parts of a tile (in dims) that its slot is handed on in: QK^T begins with the first
+// while the second is converted, and the tile after the next is converted into what PV has read
+// first. (Two parts take a tile from 1.8 to 1.6 us; a CTA of two tiles, as clusters of
+// eight have them, is faster in one part: 10.8 us where two take 11.1.)
+template <int kParts>
 __global__ void __launch_bounds__(kThreads, 1)
     attn4_kernel(AttnArgs a, const __grid_constant__ CUtensorMap qmap) {
   extern __shared__ uint8_t smem_raw[];
@@ -204,8 +209,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&misc->kv_full[i], kLoadWarps);
-      mbar_init(&misc->kv_empty[i], 1);
+      for (int p = 0; p < kParts; ++p) {
+        mbar_init(&misc->kv_full[i][p], kLoadWarps);
+        mbar_init(&misc->kv_empty[i][p], 1);
+      }
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&misc->s_full[i], 1);
@@ -383,29 +390,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Converts tile `done` into its slot.
     auto convert = [&](const uint4 (&code)[4], const uint4& scales) {
       const int sl = done % kSlots;
-      if (done >= kSlots && !wait_bar(&misc->kv_empty[sl],
-                                      static_cast<uint32_t>(((done / kSlots) - 1) & 1), misc,
-                                      a.status)) {
-        ok = false;
-        return;
-      }
       const uint32_t slot = static_cast<uint32_t>(sl * kSlotBytes);
       const uint32_t sw[4] = {scales.x, scales.y, scales.z, scales.w};
       // (a warp past the last step of 16 rows has nothing that PV reads)
-      if (8 * (w & ~1) < n_rows_cta - done * kRows) {
+      const bool needed = 8 * (w & ~1) < n_rows_cta - done * kRows;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {  // piece g + 4 i: its scale is byte g of word i
-          const uint32_t f = mx4_scale_bf16x2((sw[i] >> (8u * g)) & 0xFFu);
-          const uint32_t cw[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+      for (int p = 0; p < kParts; ++p) {
+        if (done >= kSlots && !wait_bar(&misc->kv_empty[sl][p],
+                                        static_cast<uint32_t>(((done / kSlots) - 1) & 1), misc,
+                                        a.status)) {
+          ok = false;
+          return;
+        }
+        if (needed) {
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            st_shared_v4(to[n] + slot + 2 * i * kAtomBytes, mx4_decode8(cw[n], f));
+          for (int i = p * (4 / kParts); i < (p + 1) * (4 / kParts); ++i) {
+            // piece g + 4 i: its scale is byte g of word i
+            const uint32_t f = mx4_scale_bf16x2((sw[i] >> (8u * g)) & 0xFFu);
+            const uint32_t cw[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              st_shared_v4(to[n] + slot + 2 * i * kAtomBytes, mx4_decode8(cw[n], f));
+            }
           }
         }
+        fence_proxy_async_smem();  // the MMAs read the tile through the async proxy
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&misc->kv_full[sl][p]);
       }
-      fence_proxy_async_smem();  // the MMAs read the tile through the async proxy
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&misc->kv_full[sl]);
       ++done;
     };
     // One pass: the next tile is read into one set of registers (x) while the one before it
@@ -450,17 +462,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t a_lo = lo(kv_mn) + static_cast<uint32_t>(sl * kSlotBytes >> 4);
         const int steps = (n_rows_cta - t * kRows + 15) >> 4;  // of 16 rows: those with any
 #pragma unroll 1
-        for (int m = 0; m < 4; ++m) {
+        for (int p = 0; p < kParts; ++p) {
+#pragma unroll 1
+          for (int m = p * (4 / kParts); m < (p + 1) * (4 / kParts); ++m) {
 #pragma unroll
-          for (int ks = 0; ks < kRows / 16; ++ks) {
-            mma_warp<false>(leader, tmem + kTmemO + 64 * m, a_lo + ((ks * 16 * 128) >> 4), hi(kv_mn),
-                            lo(p_k) + ((ks * 32) >> 4), hi(p_k), idesc_o,
-                            (t > 0 || ks > 0) ? 1u : 0u);
-            if (ks + 1 >= steps) break;
+            for (int ks = 0; ks < kRows / 16; ++ks) {
+              mma_warp<false>(leader, tmem + kTmemO + 64 * m, a_lo + ((ks * 16 * 128) >> 4),
+                              hi(kv_mn), lo(p_k) + ((ks * 32) >> 4), hi(p_k), idesc_o,
+                              (t > 0 || ks > 0) ? 1u : 0u);
+              if (ks + 1 >= steps) break;
+            }
+            a_lo += (2 * kAtomBytes) >> 4;
           }
-          a_lo += (2 * kAtomBytes) >> 4;
+          mma_commit_warp(leader, &misc->kv_empty[sl][p]);
         }
-        mma_commit_warp(leader, &misc->kv_empty[sl]);
         mma_commit_warp(leader, &misc->p_empty);
       }
       if (n_tiles > 0) mma_commit_warp(leader, &misc->o_done);  // every MMA has completed
@@ -469,27 +484,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool qk_ok = n_tiles == 0 || wait_bar(&misc->q_done, 0u, misc, a.status);
       for (int t = 0; t < n_tiles && qk_ok; ++t) {
         const int sl = t % kSlots, sb = t & 1;
-        if (!wait_bar(&misc->kv_full[sl], static_cast<uint32_t>((t / kSlots) & 1), misc,
-                      a.status) ||
-            (t >= 2 && !wait_bar(&misc->s_free[sb], static_cast<uint32_t>(((t >> 1) - 1) & 1),
-                                 misc, a.status))) {
-          qk_ok = false;
+        if (t >= 2 && !wait_bar(&misc->s_free[sb], static_cast<uint32_t>(((t >> 1) - 1) & 1), misc,
+                                a.status)) {
           break;
         }
-        tc_fence_after();
-        fence_proxy_async_smem();
         uint32_t a_lo = lo(q_k), b_lo = lo(kv_k) + static_cast<uint32_t>(sl * kSlotBytes >> 4);
 #pragma unroll 1
-        for (int c = 0; c < kLatent / 64; ++c) {  // atoms of 64 dims
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {
-            mma_warp<true>(leader, tmem + 32 * sb, a_lo + ((ks * 32) >> 4), hi(q_k),
-                           b_lo + ((ks * 32) >> 4), hi(kv_k), idesc_s, (c > 0 || ks > 0) ? 1u : 0u);
+        for (int p = 0; p < kParts; ++p) {
+          if (!wait_bar(&misc->kv_full[sl][p], static_cast<uint32_t>((t / kSlots) & 1), misc,
+                        a.status)) {
+            qk_ok = false;
+            break;
           }
-          a_lo += (kHeads * 128) >> 4;
-          b_lo += kAtomBytes >> 4;
+          tc_fence_after();
+          fence_proxy_async_smem();
+#pragma unroll 1
+          for (int c = 0; c < 8 / kParts; ++c) {  // atoms of 64 dims
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+              mma_warp<true>(leader, tmem + 32 * sb, a_lo + ((ks * 32) >> 4), hi(q_k),
+                             b_lo + ((ks * 32) >> 4), hi(kv_k), idesc_s,
+                             (p > 0 || c > 0 || ks > 0) ? 1u : 0u);
+            }
+            a_lo += (kHeads * 128) >> 4;
+            b_lo += kAtomBytes >> 4;
+          }
         }
-        mma_commit_warp(leader, &misc->s_full[sb]);
+        if (qk_ok) mma_commit_warp(leader, &misc->s_full[sb]);
       }
     }
     __syncwarp();
@@ -797,6 +818,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (paired && warp >= kMmaWarp) cluster_wait();
 }
 
+template <int kParts>
+cudaError_t launch_parts(const AttnArgs& a, const CUtensorMap& qmap, cudaStream_t s) {
+  static std::atomic<int> smem_set[64]{};
+  const cudaError_t e =
+      ensure_smem(reinterpret_cast<const void*>(attn4_kernel<kParts>), kSmemBytes, smem_set);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attn4_kernel<kParts>, dim3(a.B, a.splits), dim3(kThreads), kSmemBytes, s,
+                    a.splits, a, qmap);
+}
+
 }  // namespace
 
 cudaError_t launch_attn4(const AttnArgs& a, cudaStream_t s) {
@@ -811,11 +842,7 @@ cudaError_t launch_attn4(const AttnArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   AttnArgs args = a;
   args.swa_rows = static_cast<int64_t>(a.B) * a.window;
-  static std::atomic<int> smem_set[64]{};
-  e = ensure_smem(reinterpret_cast<const void*>(attn4_kernel), kSmemBytes, smem_set);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(attn4_kernel, dim3(a.B, a.splits), dim3(kThreads), kSmemBytes, s, a.splits,
-                    args, qmap);
+  return a.splits == kMaxAttnSplits ? launch_parts<1>(args, qmap, s) : launch_parts<2>(args, qmap, s);
 }
 
 }  // namespace dsa
