@@ -393,6 +393,22 @@ def test_rows_written_and_read(fmt, n, n_rows):
     assert dsa.read_device_status(ws)[0] == 0
 
 
+@pytest.mark.parametrize("scale", [2.0 ** -6, 1.0 / 3, 0.0173, 1.9999999, 3e-5, 448.0, 2.0 ** -60 * 1.3,
+                                   2.0 ** 59 * 1.7, 2.0 ** -61, 2.0 ** 61 * 1.1, 1.2e-38])
+def test_e4m3_rows_of_every_bf16_value(scale):
+    """Every finite bf16 value over a scale is the fp32 quotient's code (the scales on both
+    sides of what the reciprocal is used for)."""
+    x = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    x = torch.where(torch.isfinite(x.float()), x, torch.zeros_like(x)).view(128, 512)
+    cfg = dsa.config(kv_fmt=dsa.KV_FP8_E4M3, kv_scale=scale)
+    cache = torch.zeros((128, 512), dtype=torch.uint8, device="cuda")
+    dsa.kv_write(cfg, x.cuda(), i32(np.arange(128)), cache, small_ws())
+    with np.errstate(over="ignore", under="ignore"):
+        q = x.float().numpy() / np.float32(cfg.kv_scale)
+    want = O.e4m3_encode(np.clip(q, -1e4, 1e4).astype(np.float64))  # (saturates far below)
+    assert np.array_equal(cache.cpu().numpy(), want)
+
+
 def test_rows_past_the_cache_and_past_the_valid_ones():
     cfg, ws = dsa.config(kv_fmt=dsa.KV_MXFP4), small_ws()
     rows = torch.randn((6, 512), device="cuda").bfloat16()
