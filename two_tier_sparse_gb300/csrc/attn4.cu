@@ -8,8 +8,10 @@
 //                      K = the tile's rows; the KV tile is read as an MN-major operand)
 //
 // A row is 272 bytes, so a tile's rows fit in registers on their way: eight
-// loader warps read a tile's codes (16 bytes a lane: 32 elements, one scale)
-// while they convert the tile before it to bf16 into a swizzled operand slot.
+// loader warps read the next tile's codes (16 bytes a lane: 32 elements, one scale) into
+// one set of registers while they convert this tile's from another to bf16 in a swizzled
+// operand slot (with one set, read after the conversion, the loads' latency was
+// in every tile: 64 sequences took 17.5 us, 17.2 with two).
 // bf16 holds every code times every scale exactly, so Q stays as it is given
 // and the MMAs see the cache's own values.
 //
@@ -21,6 +23,13 @@
 // 64 rows a tile use the Q operand twice as well as 32. The weight-stationary
 // form's layout gives every math thread 32 scores of one head, so four warps
 // share the softmax.
+//
+// A tile takes about 3300 clocks: the loaders ~2000 to convert it (two instructions of
+// every three on the ALU pipe, at half rate) and ~650 to read the next one, the MMAs 1730 at
+// least, and shared memory ~2300 for what all of them move, so they slow one
+// another; the chain conversion - QK^T - softmax - PV over two slots is as long. 640 rows a
+// sequence: 1 sequence 10.8 us, 64 x 131072 16.6 us, 152 22.4 us (of those ~6 before the first and
+// after the last tile), 200 paged ragged 35.0 us.
 //
 // The split over a cluster of S CTAs, the lazy softmax maximum and the roles
 // are those of the attention over bf16 rows. The CTAs of a cluster exchange their

