@@ -36,7 +36,10 @@
 // (max, sum) first, so each scales its partial output by its final weight and the
 // merge is a sum. The partial outputs keep the upper 24 bits of their fp32 value
 // (sign, exponent, 15 mantissa bits), as a 16-bit and an 8-bit part: with bf16 parts
-// their rounding would add to the output's own, which is of the same size.
+// their rounding would add to the output's own, which is of the same size. The exchange is
+// bound by what an SM can send to others: 14 bytes a clock measured, by 16-byte
+// stores, bulk copies or remote loads alike (86 KB a CTA of eight: 6100 clocks; 49 KB a CTA
+// of two: 3800).
 #include <algorithm>
 #include <cstddef>
 
