@@ -232,3 +232,24 @@ def test_serving_tensors_of_two_devices_are_refused(lib):
         dsa._one_device(host, None, type("T", (), dict(get_device=lambda s: 0, device="cuda:0"))())
     dsa._one_device(host, None, meta)  # neither is on a CUDA device
     dsa.PagePool(host.view(1, 2), 64, host, state)
+
+
+def test_the_compiled_calls_leave_everything_but_the_plain_case(lib):
+    """Host tensors, and arguments that are no tensors at all, are not theirs: None, no error left
+    behind, and the binding's own checks answer."""
+    calls = dsa._load_calls()
+    cfg = dsa.config(kv_fmt=dsa.KV_MXFP4)
+    rows, slots = torch.zeros((2, 512), dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)
+    cache, ws = torch.zeros((4, 272), dtype=torch.uint8), torch.zeros(256, dtype=torch.uint8)
+    for a in ((True, cfg, rows, slots, cache, ws, None), (True, cfg, None, slots, cache, ws, None),
+              (False, 3, "x", slots, cache, ws, None), (True, cfg, rows)):
+        assert calls.rows(*a) is None
+    pool = dsa.PagePool.empty(2, 64, 2, 4, device="cpu")
+    plan = dsa.StepPlan.empty(2, 2, device="cpu")
+    assert calls.plan(cfg, slots, slots, pool._key, plan._key, ws) is None
+    assert calls.plan(cfg, None, slots, pool._key, plan._key, ws) is None
+    heads = dsa.HeadSet([dsa.Heads(rows)])
+    assert calls.norm(None, rows, heads._key, None, None) is None
+    assert calls.norm(None, 7, heads._key, None, None) is None
+    with pytest.raises(ValueError):
+        calls.init(1, 2, 3, 4)

@@ -614,3 +614,47 @@ def test_a_row_written_right_before_the_attention_is_read():
         for r, o in zip(rows, outs):
             assert (o == r[0, 0]).all()
         assert dsa.read_device_status(ws)[0] == 0
+
+
+def test_the_compiled_calls_and_the_binding_agree():
+    """The plain case in C and the binding's own path (a stream given): same results; what is not
+    plain (a stride, another type, another count, a host tensor) goes to the binding's path."""
+    calls, cfg, ws = dsa._load_calls(), dsa.config(kv_fmt=dsa.KV_MXFP4), small_ws()
+    s = torch.cuda.current_stream()
+    g = torch.Generator(device="cuda").manual_seed(8)
+    rows = torch.randn((5, 512), generator=g, device="cuda").bfloat16()
+    slots, one = i32([3, 0, -1, 6, 2]), i32([4])
+    a, b = (torch.zeros((7, 272), dtype=torch.uint8, device="cuda") for _ in range(2))
+    for valid in (None, one):
+        assert calls.rows(True, cfg, rows, slots, a, ws, valid) == 0
+        dsa.kv_write(cfg, rows, slots, b, ws, n_valid=valid, stream=s)
+        x, y = torch.zeros_like(rows), torch.zeros_like(rows)
+        assert calls.rows(False, cfg, x, slots, a, ws, valid) == 0
+        dsa.kv_read(cfg, b, slots, y, ws, n_valid=valid, stream=s)
+        assert torch.equal(a, b) and torch.equal(bits(x), bits(y))
+    wide = torch.zeros((5, 1024), dtype=torch.bfloat16, device="cuda")
+    for bad in ((wide[:, :512], slots, a, ws, None), (rows.float(), slots, a, ws, None),
+                (rows, slots.long(), a, ws, None), (rows, slots[:4], a, ws, None),
+                (rows, slots, a[:, :256], ws, None), (rows, slots, a, ws.cpu(), None),
+                (rows, slots, a, ws, slots), (rows, slots, a.view(-1), ws, None)):
+        assert calls.rows(True, cfg, *bad) is None
+    assert calls.rows(True, cfg, rows, slots, a, ws[8:], None) == 2  # the library's own answer
+    x = torch.randn((5, 3, 64), generator=g, device="cuda")
+    p, q = torch.zeros_like(x), torch.zeros_like(x)
+    f = dsa.Rope(torch.tensor(frequencies(16), device="cuda"))
+    hp, hq = (dsa.HeadSet([dsa.Heads(x, o, rope_start=0)]) for o in (p, q))
+    assert calls.norm(slots, x, hp._key, f._key, one) == 0
+    dsa.norm_rope(slots, hq, f, n_valid=one, stream=s)
+    assert torch.equal(p, q) and p[:4].any() and not p[4].any()
+    assert calls.norm(None, x, hp._key, f._key, None) is None
+    assert calls.norm(slots.long(), x, hp._key, f._key, None) is None
+    pools = [dsa.PagePool.empty(2, 64, 2, 4) for _ in range(2)]
+    plans = [dsa.StepPlan.empty(2, 200) for _ in range(2)]
+    n, new = i32([0, 0]), i32([100, 70])
+    assert calls.plan(cfg, n, new, pools[0]._key, plans[0]._key, ws) == 0
+    dsa.plan_step(cfg, n, new, pools[1], plans[1], ws, stream=s)
+    for k in ("n_tokens", "n_latents", "swa_len", "cu_new", "positions", "latent_slots"):
+        assert torch.equal(getattr(plans[0], k), getattr(plans[1], k)), k
+    assert torch.equal(pools[0].table, pools[1].table)
+    assert calls.plan(cfg, n[:1], new, pools[0]._key, plans[0]._key, ws) is None
+    assert dsa.read_device_status(ws)[0] == 0

@@ -9,6 +9,8 @@ call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import math
 import os
 from dataclasses import dataclass
@@ -153,6 +155,26 @@ def load() -> ctypes.CDLL:
                 getattr(lib, f).restype = ctypes.c_int
         _lib = lib
     return _lib
+
+
+_calls = None
+
+
+def _load_calls():
+    """The compiled part of the binding (csrc/calls.c), with the library's addresses."""
+    global _calls
+    lib = load()
+    path = os.path.join(os.path.dirname(LIB_PATH), "_calls.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing: build it with `python -m two_tier_sparse_gb300.build`")
+    loader = importlib.machinery.ExtensionFileLoader("_calls", path)
+    m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_calls", loader))
+    loader.exec_module(m)
+    m.init(tuple(ctypes.cast(f, ctypes.c_void_p).value for f in
+                 (lib.dsa_plan_step, lib.dsa_norm_rope, lib.dsa_kv_write, lib.dsa_kv_read)),
+           (torch.int32, torch.bfloat16, torch.int16), torch._C._cuda_getDevice, _raw_stream)
+    _calls = m
+    return m
 
 
 def _check(code: int, where: str) -> None:
@@ -381,6 +403,7 @@ class PagePool:
         self.c = _PagePool(table.data_ptr(), page_rows, table.shape[1], free_ring.shape[0],
                            free_ring.data_ptr(), ring_state.data_ptr(), out.data_ptr())
         self._ref = ctypes.byref(self.c)
+        self._key = ctypes.addressof(self.c), self.B, table.get_device()
 
     @classmethod
     def empty(cls, B: int, page_rows: int, pages_per_seq: int, n_pages: int, device="cuda"):
@@ -415,6 +438,7 @@ class StepPlan:
                            cu_new.data_ptr(), token_seq.data_ptr(), positions.data_ptr(),
                            latent_slots.data_ptr(), window_slots.data_ptr(), m)
         self._ref = ctypes.byref(self.c)
+        self._key = ctypes.addressof(self.c), B, n_tokens.get_device()
 
     @classmethod
     def empty(cls, B: int, max_new: int, device="cuda", n_tokens=None):
@@ -433,6 +457,10 @@ class StepPlan:
 def plan_step(cfg, n_tokens, n_new, pool: PagePool, plan: StepPlan, ws, stream=None):
     """Block table and slot maps of a step (dsa_plan_step): n_tokens [B] lengths
     before the step, n_new [B] tokens added (negative: the request ends)."""
+    if stream is None:  # the plain case (None: any other)
+        code = (_calls or _load_calls()).plan(cfg, n_tokens, n_new, pool._key, plan._key, ws)
+        if code is not None:
+            return _check(code, "dsa_plan_step")
     B, i32 = plan.B, torch.int32
     if n_tokens.dtype is not i32 or n_new.dtype is not i32 or n_tokens.shape != plan.shape or \
             n_new.shape != plan.shape or pool.B != B or \
@@ -496,6 +524,8 @@ class HeadSet:
         self.n, self.dtype = groups[0].n, groups[0].dtype
         self.x, self.shape, self.count = groups[0].x, groups[0].x.shape[:1], len(groups)
         self._c = (_HeadsC * len(groups))(*[g.c for g in groups])
+        self._key = (ctypes.addressof(self._c), self.count, self.n, self.dtype,
+                     self.x.get_device())
 
 
 class Rope:
@@ -509,11 +539,17 @@ class Rope:
         self.inv_freq = inv_freq
         self.c = _RopeC(inv_freq.data_ptr(), 2 * inv_freq.shape[0], int(interleaved), scale)
         self._ref = ctypes.byref(self.c)
+        self._key = ctypes.addressof(self.c), inv_freq.get_device()
 
 
 def norm_rope(positions, heads: HeadSet, rope: Optional[Rope] = None, n_valid=None, stream=None):
     """Norms of heads and their rotation in one pass (dsa_norm_rope): positions int32
     [n]; n_valid: device int32 [1], tokens behind it are left as they were."""
+    if stream is None:
+        code = (_calls or _load_calls()).norm(positions, heads.x, heads._key,
+                                              None if rope is None else rope._key, n_valid)
+        if code is not None:
+            return _check(code, "dsa_norm_rope")
     n = heads.n
     if rope is not None or positions is not None:
         if positions is None or positions.dtype is not torch.int32 or \
@@ -574,12 +610,20 @@ def kv_write(cfg, rows, slots, cache, ws, n_valid=None, stream=None):
     """bf16 rows [n, 512] into a cache of cfg.kv_fmt (dsa_kv_write): row r becomes cache
     row slots[r], negative slots skip; cache: [..., row] contiguous (a pool of pages, or
     the window rows)."""
+    if stream is None:
+        code = (_calls or _load_calls()).rows(True, cfg, rows, slots, cache, ws, n_valid)
+        if code is not None:
+            return _check(code, "dsa_kv_write")
     _rows_call("dsa_kv_write", cfg, rows, slots, cache, ws, n_valid, stream)
 
 
 def kv_read(cfg, cache, slots, rows, ws, n_valid=None, stream=None):
     """Rows slots[r] of a cache back as bf16 rows [n, 512] (dsa_kv_read); rows with a
     negative slot are left as they were."""
+    if stream is None:
+        code = (_calls or _load_calls()).rows(False, cfg, rows, slots, cache, ws, n_valid)
+        if code is not None:
+            return _check(code, "dsa_kv_read")
     _rows_call("dsa_kv_read", cfg, rows, slots, cache, ws, n_valid, stream)
 
 

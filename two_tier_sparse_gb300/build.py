@@ -1,7 +1,8 @@
 """Builds libdsa.so (the C-ABI library of include/dsa.h) in-tree with nvcc for sm_103a.
 
 Each .cu file under csrc/ compiles in parallel to an object under _build/,
-then nvcc links them into two_tier_sparse_gb300/libdsa.so. No CMake.
+then nvcc links them into two_tier_sparse_gb300/libdsa.so. The binding's own compiled part
+(csrc/calls.c, a CPython module) goes to two_tier_sparse_gb300/_calls.so. No CMake.
 """
 from __future__ import annotations
 
@@ -10,12 +11,14 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdsa.so")
+CALLS = os.path.join(PKG, "_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -66,7 +69,19 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         tmp = LIB + f".tmp{os.getpid()}"
         subprocess.check_call([nvcc, *ARCH, "-shared", "-o", tmp, *objs])
         os.replace(tmp, LIB)
+    build_calls(force)
     return LIB
+
+
+def build_calls(force: bool = False) -> str:
+    src = os.path.join(CSRC, "calls.c")
+    if force or _stale(CALLS, [src, os.path.join(ROOT, "include", "dsa.h")]):
+        tmp = CALLS + f".tmp{os.getpid()}"
+        subprocess.check_call(["gcc", "-O2", "-Wall", "-shared", "-fPIC",
+                               "-I" + sysconfig.get_paths()["include"],
+                               "-I" + os.path.join(ROOT, "include"), src, "-o", tmp])
+        os.replace(tmp, CALLS)
+    return CALLS
 
 
 if __name__ == "__main__":
