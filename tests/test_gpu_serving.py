@@ -658,3 +658,31 @@ def test_the_compiled_calls_and_the_binding_agree():
     assert torch.equal(pools[0].table, pools[1].table)
     assert calls.plan(cfg, n[:1], new, pools[0]._key, plans[0]._key, ws) is None
     assert dsa.read_device_status(ws)[0] == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("dim,interleaved", [(128, True), (256, False), (512, True), (512, False),
+                                             (576, False), (1024, True)])
+def test_norm_rope_runs_over_many_units(dtype, dim, interleaved):
+    """Calls of many more units than warps: a warp's run goes over heads, groups and tokens, with
+    odd head counts (a warp's last heads missing), a group that is only rotated and one
+    that is only normed, and tokens behind the last valid one."""
+    n, valid, rope_dim = 800, 787, 64
+    g = torch.Generator(device="cuda").manual_seed(dim + interleaved)
+    f = frequencies(rope_dim // 2)
+    pos = torch.randint(0, 1 << 20, (n,), generator=g, device="cuda").to(torch.int32)
+    specs = [(11, dim, dim - 64, True), (1, dim, None, True), (5, 128, 64, True), (3, 72, 8, False)]
+    groups, given = [], []
+    for heads, d, start, norm in specs:
+        x = torch.randn((n, heads, d), generator=g, device="cuda").to(dtype)
+        w = torch.randn((d,), generator=g, device="cuda") if norm else None
+        out = torch.full_like(x, 7.0)
+        groups.append(dsa.Heads(x, out, weight=w, eps=1e-6, norm=norm, rope_start=start))
+        given.append((x, out, w, start, norm))
+    dsa.norm_rope(pos, dsa.HeadSet(groups), dsa.Rope(torch.tensor(f, device="cuda"),
+                                                     interleaved=interleaved, scale=1.25),
+                  n_valid=i32([valid]))
+    for x, out, w, start, norm in given:
+        assert (out[valid:] == 7.0).all()
+        check_heads(out[:valid], x[:valid], w, float(np.float32(1e-6)), pos[:valid].cpu().numpy(), f,
+                    -1 if start is None else start, interleaved, 1.25, norm=norm)
