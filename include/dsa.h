@@ -493,8 +493,12 @@ typedef struct {
  * free pages are too few or the ring's counters are not those of a ring, the
  * call changes no length, no table entry and nothing of the ring, cu_new is 0,
  * every token entry is that of a row past the last token, and
- * dsa_read_device_status reports DSA_ERR_DEVICE_CHECK. A table entry outside
- * the pool gives -1 slots and is reported, too.
+ * dsa_read_device_status reports DSA_ERR_DEVICE_CHECK.
+ * A page id outside the pool (0 .. n_pages - 1) is not passed on; -1, no page, takes its
+ * place. Tokens that fall on such an entry, of the table or newly popped from the ring, get -1
+ * slots and are reported with their request, in whose row the ring's entry is -1. When a
+ * request ends that holds such an entry, the request is reported, and the page's position in
+ * the ring holds -1 (an entry that is -1 already goes back as it is: its tokens were reported).
  * B is at most DSA_PLAN_MAX_REQUESTS (DSA_ERR_UNSUPPORTED above). The workspace
  * may be of any size that dsa_workspace_size gives.
  */

@@ -9,7 +9,8 @@
 // that a request gains in this step is known from the prefix sums and the
 // ring, so a token's slot never reads a table entry that this launch writes.
 // Popped and pushed positions of the ring never meet: free pages and pushed
-// ones together are at most the pool, the ring's size. What may be updated in
+// ones together are at most the pool, the ring's size. An id outside the pool moves
+// neither way: -1 takes its place. What may be updated in
 // place (lengths, the ring's counters) is written by the last CTA to finish,
 // when all have read it. The work is a few integer operations a token and four
 // words written, so a small step costs its launch and two dependent reads: the
@@ -168,18 +169,23 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
     const int64_t i = int64_t{base} + k;
     return static_cast<int>(i >= a.n_pages ? i - a.n_pages : i);
   };
+  auto in_pool = [&](int page) -> bool { return page >= 0 && page < a.n_pages; };
 
   // The table's new entries, and the pages of ended requests back to the ring: from the
   // grid's last thread down, so that in a small step they fall to other warps than the
   // tokens.
   for (int k = gstep - 1 - gtid; k < n_pop; k += gstep) {
     const int b = find(pop, a.B, k);
-    a.table[static_cast<int64_t>(b) * a.pages_per_seq + held[b] + (k - pop[b])] =
-        a.ring[ring_at(head_m, k)];
+    const int pg = a.ring[ring_at(head_m, k)];  // (outside the pool: its tokens report it)
+    a.table[static_cast<int64_t>(b) * a.pages_per_seq + held[b] + (k - pop[b])] = in_pool(pg) ? pg : -1;
   }
   for (int k = gstep - 1 - gtid; k < n_push; k += gstep) {
     const int b = find(push, a.B, k);
-    a.ring[ring_at(tail_m, k)] = a.table[static_cast<int64_t>(b) * a.pages_per_seq + (k - push[b])];
+    const int pg = a.table[static_cast<int64_t>(b) * a.pages_per_seq + (k - push[b])];
+    a.ring[ring_at(tail_m, k)] = in_pool(pg) ? pg : -1;
+    if (!in_pool(pg) && pg != -1) {
+      record_status(a.status, DSA_ERR_DEVICE_CHECK, SITE_PLAN, static_cast<uint32_t>(b));
+    }
   }
 
   // Tokens: kPer consecutive ones a thread; rows past the last token are empty.
@@ -212,7 +218,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       if (lslot[k] >= 0) {
-        if (page[k] >= 0 && page[k] < a.n_pages) {
+        if (in_pool(page[k])) {
           lslot[k] += page[k] * R;
         } else {
           lslot[k] = -1;
