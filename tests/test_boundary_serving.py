@@ -253,3 +253,17 @@ def test_the_compiled_calls_leave_everything_but_the_plain_case(lib):
     assert calls.norm(None, 7, heads._key, None, None) is None
     with pytest.raises(ValueError):
         calls.init(1, 2, 3, 4)
+
+
+@pytest.mark.parametrize("dim,rope_dim", [(128, 64), (64, 64), (1024, 1024), (32, 64)])
+def test_rotations_that_start_past_the_head_are_refused(lib, dim, rope_dim):
+    """Starts up to the largest multiple of 8 that an int holds: start + rope_dim may pass 2^31."""
+    rope = dsa._RopeC(inv_freq=A, rope_dim=rope_dim, interleaved=1, scale=1.0)
+    last = dim - rope_dim
+    for start in (last + 8, 1 << 20, (1 << 31) - rope_dim - 8, (1 << 31) - rope_dim, (1 << 31) - 8):
+        if start < 0:
+            continue
+        h = dsa._HeadsC(x=A, out=A, heads=2, dim=dim, x_token_stride=2 * dim, x_head_stride=dim,
+                        out_token_stride=2 * dim, out_head_stride=dim, weight=A, eps=1e-6, norm=1,
+                        rope_start=start)
+        assert lib.dsa_norm_rope(4, None, A, 0, ctypes.byref(h), 1, ctypes.byref(rope), None) == 1, start

@@ -1116,7 +1116,7 @@ dsa_status_t dsa_norm_rope(int n, const int32_t* n_valid, const int32_t* positio
     if (h.heads < 0 || h.dim < 8 || h.dim > 1024 || h.dim % 8 != 0) return DSA_ERR_INVALID_ARG;
     if (h.norm && !(h.eps >= 0.f && isfinite(h.eps))) return DSA_ERR_INVALID_ARG;
     if (h.rope_start >= 0 &&
-        (rope == nullptr || h.rope_start % 8 != 0 || h.rope_start + rope->rope_dim > h.dim)) {
+        (rope == nullptr || h.rope_start % 8 != 0 || h.rope_start > h.dim - rope->rope_dim)) {
       return DSA_ERR_INVALID_ARG;
     }
     if (h.heads == 0 || n == 0) continue;
