@@ -533,7 +533,8 @@ typedef struct {
 /* A rotation: pair i of a token at position p turns by p * inv_freq[i]; cosine
  * and sine are multiplied by `scale` (1 for plain RoPE, YaRN's factor with it). */
 typedef struct {
-  const double* inv_freq;    /* device fp64 [rope_dim / 2], radians per position */
+  const double* inv_freq;    /* device fp64 [rope_dim / 2], radians per position, of either
+                                sign; an infinity or NaN makes its pair NaN */
   int rope_dim;              /* rotated elements: a multiple of 8 (interleaved) or 16, <= 1024 */
   int interleaved;           /* pair i: elements 2i and 2i + 1; else i and i + rope_dim / 2 */
   float scale;
@@ -547,9 +548,11 @@ typedef struct {
  *     then elements rope_start .. rope_start + rope_dim - 1 turned in pairs:
  *     (y0, y1) -> (y0 c - y1 s, y0 s + y1 c).
  * The pages name a KV norm and RoPE (theta 160000, YaRN x16) and give no
- * formula; RMS norm and both pairings are the common forms. Arithmetic in fp32
- * (angles in fp64), one rounding to the elements' type.
- *   positions: device int32 [n]
+ * formula; RMS norm and both pairings are the common forms. Arithmetic in fp32,
+ * one rounding to the elements' type. An angle p * inv_freq[i] is reduced to its fraction of
+ * a turn in 64-bit integers, right to within 2^-33 turns and 2^-63 of the whole
+ * angle, and its cosine and sine are taken in fp32.
+ *   positions: device int32 [n], of either sign
  *   n_valid:   device int32 or NULL: only tokens below *n_valid are done, the
  *              rows behind them are left as they were (cu_new + B of a plan)
  *   groups:    host array of n_groups <= DSA_MAX_HEAD_GROUPS

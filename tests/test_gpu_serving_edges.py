@@ -1,10 +1,13 @@
-"""Edges of the serving calls on the GPU: page ids that are no pages."""
+"""Edges of the serving calls on the GPU: page ids that are no pages, frequencies and positions
+of any size. Tolerances as in test_gpu_serving.py, where nothing else is said."""
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
 
 import two_tier_sparse_gb300 as dsa
-from test_gpu_serving import i32, small_ws
+from test_gpu_serving import frequencies, i32, small_ws
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +76,72 @@ def test_a_ring_entry_outside_the_pool_gives_no_page(bad):
     assert pool.ring_state.tolist() == [4, 11]
     assert [int(pool.free_ring[i % 8]) for i in range(4, 11)] == [4, 5, 6, 7, -1, 2, 3]
     assert dsa.read_device_status(ws)[0] == 0
+
+
+TWO_PI = Fraction("6.283185307179586476925286766559005768394338798750211641949889184615632812572417997256069650684234136")
+
+
+def exact_rotation(x, pos, f, start, interleaved):
+    """Pairs of x [n, heads, dim] (float64) turned by pos * f, each angle reduced exactly."""
+    y = np.array(x, np.float64)
+    half = len(f)
+    i = np.arange(half)
+    i0, i1 = (start + 2 * i, start + 2 * i + 1) if interleaved else (start + i, start + half + i)
+    a = np.empty((len(pos), half))
+    for t, p in enumerate(pos):
+        for k, g in enumerate(f):
+            turns = int(p) * Fraction(float(g)) / TWO_PI
+            a[t, k] = float((turns - round(turns)) * TWO_PI)
+    c, s = np.cos(a)[:, None], np.sin(a)[:, None]
+    y0, y1 = y[..., i0], y[..., i1]
+    y[..., i0], y[..., i1] = y0 * c - y1 * s, y0 * s + y1 * c
+    size = np.abs(np.array(x, np.float64))
+    size[..., i0] = size[..., i1] = np.abs(y0) + np.abs(y1)
+    return y, size
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+def test_norm_rope_frequencies_and_positions_of_any_size(interleaved):
+    """Frequencies above a turn a position, negative ones, subnormal ones and zero, and negative
+    positions: an angle is off by at most 2^-33 turns (under 2^-30 radians) + |angle| 2^-62, the
+    rest as above."""
+    rng = np.random.default_rng(4)
+    f = np.array([2 * np.pi, 6.2831853071795871, 7.5, 100.25, 9999.875, -3.25, -1e4, 2.0 ** 30,
+                  0.0, 5e-324, 1e-310, 1.0, 160000.0 ** -0.5, 1e-9, 3e5, 2.0 ** -40])
+    pos = np.array([0, 1, -1, 5, -77777, 2 ** 20, 2 ** 31 - 1, -2 ** 31])
+    x = rng.standard_normal((len(pos), 3, 64)).astype(np.float32)
+    want, size = exact_rotation(x, pos, f, 32, interleaved)
+    out = torch.empty((len(pos), 3, 64), device="cuda")
+    heads = dsa.Heads(torch.from_numpy(x).cuda(), out, norm=False, rope_start=32)
+    dsa.norm_rope(i32(pos), dsa.HeadSet([heads]), dsa.Rope(torch.tensor(f, device="cuda"),
+                                                           interleaved=interleaved))
+    # the angles' error, for each pair
+    off = 2.0 ** -30 + np.abs(pos[:, None].astype(np.float64) * f) * 2.0 ** -62
+    i = np.arange(16)
+    i0, i1 = (32 + 2 * i, 33 + 2 * i) if interleaved else (32 + i, 48 + i)
+    tol = 2.0 ** -24 * np.abs(want) * (1 + 2.0 ** -10) + 2.0 ** -19 * size
+    tol[..., i0] += off[:, None] * size[..., i0]
+    tol[..., i1] += off[:, None] * size[..., i1]
+    assert np.all(np.abs(out.double().cpu().numpy() - want) <= tol)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("interleaved", [True, False])
+def test_norm_rope_frequencies_that_are_no_numbers(interleaved, dtype):
+    """An infinite or NaN frequency has no angle: its pair is NaN, in every head and at every
+    position, and the other pairs are as without it."""
+    f = frequencies(16)
+    x = torch.randn((4, 3, 64), device="cuda").to(dtype)
+    outs = []
+    for bad in ((), (2, 7, 11)):
+        g = f.copy()
+        g[list(bad)] = [float("inf"), float("nan"), -float("inf")][:len(bad)]
+        out = torch.empty_like(x)
+        dsa.norm_rope(i32([0, 1, 5, -3]), dsa.HeadSet([dsa.Heads(x, out, rope_start=32)]),
+                      dsa.Rope(torch.tensor(g, device="cuda"), interleaved=interleaved))
+        outs.append(out)
+    nan = torch.zeros(64, dtype=torch.bool, device="cuda")
+    for k in (2, 7, 11):
+        nan[[32 + 2 * k, 33 + 2 * k] if interleaved else [32 + k, 48 + k]] = True
+    assert torch.equal(outs[1].isnan(), nan.expand(4, 3, 64))
+    assert torch.equal(outs[1][..., ~nan], outs[0][..., ~nan])

@@ -530,7 +530,7 @@ class HeadSet:
 
 class Rope:
     """A rotation (dsa_rope_t): inv_freq fp64 [rope_dim / 2] on the device, radians per
-    position; interleaved pairs (2i, 2i + 1) or halves (i, i + rope_dim / 2); cosine
+    position (finite; an infinity or NaN makes its pair NaN); interleaved pairs (2i, 2i + 1) or halves (i, i + rope_dim / 2); cosine
     and sine times scale."""
 
     def __init__(self, inv_freq: torch.Tensor, interleaved: bool = True, scale: float = 1.0):

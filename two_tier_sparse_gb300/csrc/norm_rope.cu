@@ -110,8 +110,8 @@ __device__ __forceinline__ void ld_shared_f2x2(uint32_t at, F2& a, F2& b) {
 // f / (2 pi) in units of 2^-64 turns, modulo whole turns, rounded down: the fp64 number
 // f = m 2^(e - 1075) with its 53-bit integer m, times 1 / (2 pi) = inv_2pi 2^-66 (inv_2pi
 // the 64-bit integer), is m inv_2pi 2^(e - 1077) of those units. A position times this,
-// modulo 2^64, is the angle's fraction of a turn to within 2^-33 (positions below 2^31,
-// frequencies of at most a turn a position).
+// modulo 2^64, is the angle's fraction of a turn to within 2^-33 and 2^-63 of the angle in turns
+// (positions of either sign). f is finite: an infinity or NaN has no angle, see angle_exists.
 __device__ __forceinline__ uint64_t turn_bits(double f, uint64_t inv_2pi) {
   const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(f));
   const int e = static_cast<int>(bits >> 52) & 0x7FF;
@@ -127,6 +127,10 @@ __device__ __forceinline__ uint64_t turn_bits(double f, uint64_t inv_2pi) {
     t = sh > -64 ? lo << -sh : 0ull;
   }
   return static_cast<int64_t>(bits) < 0 ? 0ull - t : t;
+}
+
+__device__ __forceinline__ bool angle_exists(double f) {
+  return (static_cast<uint32_t>(__double_as_longlong(f) >> 52) & 0x7FFu) != 0x7FFu;
 }
 
 // Shared memory of a warp's cosines and sines: (cos, sin) of each pair, or (halves) the
@@ -264,9 +268,12 @@ __global__ void __launch_bounds__(32 * kWarps, NV == 1 ? 3 : NV == 2 ? 2 : 1)
       const int64_t pos = a.positions[tok];
       __syncwarp();
       for (int k = lane; k < pairs; k += 32) {
-        const int64_t turn = pos * static_cast<int64_t>(turn_bits(a.inv_freq[k], a.inv_2pi));
+        const double f = a.inv_freq[k];
+        const int64_t turn = pos * static_cast<int64_t>(turn_bits(f, a.inv_2pi));
         float sn, cs;
-        sincospif(static_cast<float>(turn) * 0x1p-63f, &sn, &cs);  // half turns, from -1 to 1
+        sincospif(angle_exists(f) ? static_cast<float>(turn) * 0x1p-63f  // half turns, from -1 to 1
+                                  : __int_as_float(0x7FC00000),          // (NaN)
+                  &sn, &cs);
         cs *= a.rope_scale;
         sn *= a.rope_scale;
         if (a.interleaved) {
