@@ -1,0 +1,55 @@
+"""What the Python package needs to be imported, built and used: a torch without CUDA, a
+machine without the Python headers, a binding without its compiled part (no compute call
+runs here)."""
+import os
+import subprocess
+import sys
+import textwrap
+
+import pytest
+import torch
+
+import two_tier_sparse_gb300 as dsa
+from two_tier_sparse_gb300 import build as dsa_build
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    dsa_build.build()
+    dsa.load()
+
+
+def host_calls_are_refused():
+    """Host tensors to every call that the compiled part takes: the binding's own answer."""
+    i = dict(dtype=torch.int32)
+    x, slots = torch.zeros((2, 512), dtype=torch.bfloat16), torch.zeros(2, **i)
+    cache, ws = torch.zeros((4, 512), dtype=torch.bfloat16), torch.zeros(256, dtype=torch.uint8)
+    pool, plan = dsa.PagePool.empty(2, 64, 2, 4, device="cpu"), dsa.StepPlan.empty(2, 2, device="cpu")
+    cfg = dsa.config()
+    for call in (lambda: dsa.norm_rope(None, dsa.HeadSet([dsa.Heads(x)])),
+                 lambda: dsa.kv_write(cfg, x, slots, cache, ws),
+                 lambda: dsa.kv_read(cfg, cache, slots, x, ws),
+                 lambda: dsa.plan_step(cfg, slots, slots, pool, plan, ws)):
+        with pytest.raises(ValueError, match="not the current CUDA device"):
+            call()
+
+
+def test_the_package_works_with_a_torch_without_cuda():
+    """A torch built without CUDA lacks these functions; the package imports, and its host side
+    (configurations, workspace sizes, handles, refusals) works."""
+    code = textwrap.dedent("""
+        import torch
+        for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+            if hasattr(torch._C, name):
+                delattr(torch._C, name)
+        import two_tier_sparse_gb300 as dsa
+        assert dsa.workspace_size(dsa.config(), 4, 4096) > 0
+        from test_binding_parts import host_calls_are_refused
+        host_calls_are_refused()
+        print("fine")
+    """)
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([ROOT, os.path.join(ROOT, "tests")]))
+    p = subprocess.run([sys.executable, "-c", code], env=env, cwd=ROOT, capture_output=True, text=True)
+    assert p.returncode == 0 and p.stdout.strip() == "fine", p.stderr[-2000:]

@@ -160,10 +160,23 @@ def load() -> ctypes.CDLL:
 _calls = None
 
 
+class _NoCalls:
+    """In the compiled part's place where it cannot be used: leaves every call to the binding."""
+
+    @staticmethod
+    def plan(*args):
+        return None
+
+    norm = rows = plan
+
+
 def _load_calls():
     """The compiled part of the binding (csrc/calls.c), with the library's addresses."""
     global _calls
     lib = load()
+    if _raw_stream is None:  # a torch without CUDA
+        _calls = _NoCalls
+        return _calls
     path = os.path.join(os.path.dirname(LIB_PATH), "_calls.so")
     if not os.path.exists(path):
         raise RuntimeError(f"{path} is missing: build it with `python -m two_tier_sparse_gb300.build`")
@@ -184,7 +197,8 @@ def _check(code: int, where: str) -> None:
 
 # Pointers and streams travel as plain integers (every argument is declared void*):
 # building ctypes objects for them cost more than the call itself.
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# (A torch without CUDA has no such function; no call gets as far as using it there.)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = torch.cuda.current_device
 
 
