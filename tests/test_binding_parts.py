@@ -53,3 +53,10 @@ def test_the_package_works_with_a_torch_without_cuda():
     env = dict(os.environ, PYTHONPATH=os.pathsep.join([ROOT, os.path.join(ROOT, "tests")]))
     p = subprocess.run([sys.executable, "-c", code], env=env, cwd=ROOT, capture_output=True, text=True)
     assert p.returncode == 0 and p.stdout.strip() == "fine", p.stderr[-2000:]
+
+
+def test_a_missing_compiled_part_leaves_the_calls_to_the_binding(monkeypatch, tmp_path):
+    """The four calls are complete without it: they reach their own checks (and the library)."""
+    monkeypatch.setattr(dsa, "_calls", None)
+    monkeypatch.setattr(dsa, "LIB_PATH", str(tmp_path / "libdsa.so"))  # (loaded already)
+    host_calls_are_refused()

@@ -145,3 +145,28 @@ def test_norm_rope_frequencies_that_are_no_numbers(interleaved, dtype):
         nan[[32 + 2 * k, 33 + 2 * k] if interleaved else [32 + k, 48 + k]] = True
     assert torch.equal(outs[1].isnan(), nan.expand(4, 3, 64))
     assert torch.equal(outs[1][..., ~nan], outs[0][..., ~nan])
+
+
+def test_the_calls_without_the_compiled_part(monkeypatch):
+    """Plan, norm, rows in and out through the binding alone: as with the compiled part."""
+    calls, plain = dsa._load_calls(), dsa._NoCalls
+    assert calls is not plain
+    cfg, ws = dsa.config(kv_fmt=dsa.KV_MXFP4), small_ws()
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn((5, 512), generator=g, device="cuda").bfloat16()
+    rope = dsa.Rope(torch.tensor(frequencies(32), device="cuda"))
+    got = []
+    for part in (calls, plain):
+        monkeypatch.setattr(dsa, "_calls", part)
+        pool, plan = dsa.PagePool.empty(2, 64, 2, 4), dsa.StepPlan.empty(2, 5)
+        dsa.plan_step(cfg, i32([0, 0]), i32([3, 2]), pool, plan, ws)
+        y, cache = torch.zeros_like(x), torch.zeros((256, 272), dtype=torch.uint8, device="cuda")
+        dsa.norm_rope(plan.positions, dsa.HeadSet([dsa.Heads(x, y, rope_start=448)]), rope,
+                      n_valid=plan.n_valid)
+        dsa.kv_write(cfg, y, plan.latent_slots, cache, ws)
+        back = torch.zeros_like(x)
+        dsa.kv_read(cfg, cache, plan.latent_slots, back, ws)
+        got.append((pool.table, plan.latent_slots, y, cache, back))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert got[0][4].any() and dsa.read_device_status(ws)[0] == 0

@@ -171,15 +171,14 @@ class _NoCalls:
 
 
 def _load_calls():
-    """The compiled part of the binding (csrc/calls.c), with the library's addresses."""
+    """The compiled part of the binding (csrc/calls.c), with the library's addresses. It only
+    makes a plain call cheaper; without it the binding checks and passes every call itself."""
     global _calls
     lib = load()
-    if _raw_stream is None:  # a torch without CUDA
+    path = os.path.join(os.path.dirname(LIB_PATH), "_calls.so")
+    if _raw_stream is None or not os.path.exists(path):  # a torch without CUDA, or not built
         _calls = _NoCalls
         return _calls
-    path = os.path.join(os.path.dirname(LIB_PATH), "_calls.so")
-    if not os.path.exists(path):
-        raise RuntimeError(f"{path} is missing: build it with `python -m two_tier_sparse_gb300.build`")
     loader = importlib.machinery.ExtensionFileLoader("_calls", path)
     m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_calls", loader))
     loader.exec_module(m)
