@@ -60,3 +60,21 @@ def test_a_missing_compiled_part_leaves_the_calls_to_the_binding(monkeypatch, tm
     monkeypatch.setattr(dsa, "_calls", None)
     monkeypatch.setattr(dsa, "LIB_PATH", str(tmp_path / "libdsa.so"))  # (loaded already)
     host_calls_are_refused()
+
+
+@pytest.mark.parametrize("missing", ["headers", "compiler"])
+def test_the_library_builds_without_what_the_compiled_part_needs(monkeypatch, tmp_path, missing, capsys):
+    """No Python headers, or no C compiler: the library is built all the same, the compiled part
+    is left out (said on stderr), and one that no longer fits its source does not stay."""
+    if missing == "headers":
+        monkeypatch.setattr(dsa_build.sysconfig, "get_paths", lambda: {"include": str(tmp_path)})
+    else:
+        monkeypatch.setenv("PATH", str(tmp_path))
+    old = tmp_path / "old.so"
+    old.write_bytes(b"old")
+    os.utime(old, (0, 0))
+    monkeypatch.setattr(dsa_build, "CALLS", str(old))
+    assert dsa_build.build() == dsa_build.LIB
+    assert not old.exists()
+    assert "calls.c" in capsys.readouterr().err
+    dsa_build.build()  # and again, with none there

@@ -2,13 +2,15 @@
 
 Each .cu file under csrc/ compiles in parallel to an object under _build/,
 then nvcc links them into two_tier_sparse_gb300/libdsa.so. The binding's own compiled part
-(csrc/calls.c, a CPython module) goes to two_tier_sparse_gb300/_calls.so. No CMake.
+(csrc/calls.c, a CPython module) goes to two_tier_sparse_gb300/_calls.so where the Python headers
+are there, and is left out elsewhere. No CMake.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -73,12 +75,19 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     return LIB
 
 
-def build_calls(force: bool = False) -> str:
+def build_calls(force: bool = False) -> str | None:
+    """The binding's compiled part. The library does not need it, and the binding works without
+    it: with no Python headers or no gcc it is left out (None), and an old one removed."""
     src = os.path.join(CSRC, "calls.c")
     if force or _stale(CALLS, [src, os.path.join(ROOT, "include", "dsa.h")]):
+        include = sysconfig.get_paths()["include"]
+        if not os.path.exists(os.path.join(include, "Python.h")) or shutil.which("gcc") is None:
+            sys.stderr.write(f"csrc/calls.c is left out: it needs gcc and {include}/Python.h\n")
+            if os.path.exists(CALLS):
+                os.remove(CALLS)
+            return None
         tmp = CALLS + f".tmp{os.getpid()}"
-        subprocess.check_call(["gcc", "-O2", "-Wall", "-shared", "-fPIC",
-                               "-I" + sysconfig.get_paths()["include"],
+        subprocess.check_call(["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I" + include,
                                "-I" + os.path.join(ROOT, "include"), src, "-o", tmp])
         os.replace(tmp, CALLS)
     return CALLS
