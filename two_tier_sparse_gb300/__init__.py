@@ -175,7 +175,8 @@ def _load_calls():
     makes a plain call cheaper; without it the binding checks and passes every call itself."""
     global _calls
     lib = load()
-    path = os.path.join(os.path.dirname(LIB_PATH), "_calls.so")
+    path = os.path.join(os.path.dirname(LIB_PATH),
+                        "_calls" + importlib.machinery.EXTENSION_SUFFIXES[0])
     if _raw_stream is None or not os.path.exists(path):  # a torch without CUDA, or not built
         _calls = _NoCalls
         return _calls

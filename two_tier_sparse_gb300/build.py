@@ -2,13 +2,14 @@
 
 Each .cu file under csrc/ compiles in parallel to an object under _build/,
 then nvcc links them into two_tier_sparse_gb300/libdsa.so. The binding's own compiled part
-(csrc/calls.c, a CPython module) goes to two_tier_sparse_gb300/_calls.so where the Python headers
-are there, and is left out elsewhere. No CMake.
+(csrc/calls.c, a CPython module) goes to two_tier_sparse_gb300/_calls.<tag>.so where the Python
+headers are there, and is left out elsewhere. No CMake.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.machinery
 import os
 import shutil
 import subprocess
@@ -20,7 +21,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdsa.so")
-CALLS = os.path.join(PKG, "_calls.so")
+# (the interpreter's tag in its name: a module of one Python is not for another)
+CALLS = os.path.join(PKG, "_calls" + importlib.machinery.EXTENSION_SUFFIXES[0])
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
