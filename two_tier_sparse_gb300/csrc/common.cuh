@@ -92,12 +92,6 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   return v;
 }
 
-__device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
-  return v;
-}
-
 // Four fp32 values from shared memory (no compiler memory barrier: callers
 // order it against writes with a named barrier or __syncthreads).
 __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
