@@ -566,7 +566,7 @@ dsa_status_t dsa_norm_rope(int n, const int32_t* n_valid, const int32_t* positio
  * Rows into a cache: bf16 row r of `rows` (r * row_stride elements from its
  * start) becomes row slots[r] of `cache` in cfg->kv_fmt.
  *   DSA_KV_BF16: as it is. DSA_KV_FP8_E4M3: RN_e4m3(x / kv_scale, divided in fp32),
- *   saturating.
+ *   saturating: an infinity becomes +-448, a NaN a NaN code.
  *   DSA_KV_MXFP4: the OCP MX conversion (scale 2^X, X = floor(log2 amax) - 2 per
  *   32 elements, at least -127; 2^0 for zeros; elements to nearest, ties to the
  *   even code, at most 6); a group that holds a NaN or an infinity gets the NaN

@@ -1,5 +1,5 @@
 """Edges of the serving calls on the GPU: page ids that are no pages, frequencies and positions
-of any size. Tolerances as in test_gpu_serving.py, where nothing else is said."""
+of any size, cache elements that are no numbers. Tolerances as in test_gpu_serving.py, where nothing else is said."""
 from fractions import Fraction
 
 import numpy as np
@@ -170,3 +170,28 @@ def test_the_calls_without_the_compiled_part(monkeypatch):
     for a, b in zip(*got):
         assert torch.equal(a, b)
     assert got[0][4].any() and dsa.read_device_status(ws)[0] == 0
+
+
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** -6, 0.0173, 2.0 ** -61, 2.0 ** 61 * 1.1])
+def test_e4m3_rows_of_nan_and_infinity(scale):
+    """A NaN becomes a NaN code and an infinity the largest number, on both sides of what the
+    reciprocal is used for; the elements beside them are as without them."""
+    rows = torch.randn((2, 512), device="cuda").bfloat16()
+    cfg, ws = dsa.config(kv_fmt=dsa.KV_FP8_E4M3, kv_scale=scale), small_ws()
+    clean, cache = (torch.zeros((2, 512), dtype=torch.uint8, device="cuda") for _ in range(2))
+    dsa.kv_write(cfg, rows, i32([0, 1]), clean, ws)
+    rows[0, 3], rows[0, 4], rows[1, 511] = float("nan"), float("inf"), -float("inf")
+    rows[1, 0] = torch.tensor([-1], dtype=torch.int16).view(torch.bfloat16)[0]  # a negative NaN
+    dsa.kv_write(cfg, rows, i32([0, 1]), cache, ws)
+    assert int(cache[0, 3]) & 0x7F == 0x7F and int(cache[1, 0]) & 0x7F == 0x7F
+    assert int(cache[0, 4]) == 0x7E and int(cache[1, 511]) == 0xFE
+    for r, c in ((0, 3), (0, 4), (1, 511), (1, 0)):
+        cache[r, c] = clean[r, c]
+    assert torch.equal(cache, clean)
+    dsa.kv_write(cfg, rows, i32([0, 1]), cache, ws)
+    out = torch.zeros_like(rows)
+    dsa.kv_read(cfg, cache, i32([0, 1]), out, ws)
+    nan = torch.zeros((2, 512), dtype=torch.bool, device="cuda")
+    nan[0, 3] = nan[1, 0] = True
+    assert torch.equal(out.isnan(), nan)
+    assert dsa.read_device_status(ws)[0] == 0
