@@ -585,7 +585,8 @@ dsa_status_t dsa_kv_write(const dsa_config_t* cfg, int n, const int32_t* n_valid
 
 /*
  * Rows out of a cache: row slots[r] of `cache` as bf16 to row r of `rows`, code
- * times scale (exact for MXFP4 scales up to 2^125; rounded once for E4M3). Rows
+ * times scale (exact for MXFP4 scales up to 2^125; rounded once for E4M3, products
+ * of at least 2^-122). Rows
  * with a negative slot are left as they were. A cache of any format so serves
  * the calls that read bf16 rows (a sequence's latents for dsa_sparse_attn_prefill).
  */

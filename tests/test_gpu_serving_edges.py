@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+import oracle as O
 import two_tier_sparse_gb300 as dsa
 from test_gpu_serving import frequencies, i32, small_ws
 
@@ -194,4 +195,33 @@ def test_e4m3_rows_of_nan_and_infinity(scale):
     nan = torch.zeros((2, 512), dtype=torch.bool, device="cuda")
     nan[0, 3] = nan[1, 0] = True
     assert torch.equal(out.isnan(), nan)
+    assert dsa.read_device_status(ws)[0] == 0
+
+
+def test_e4m3_rows_read_are_rounded_once():
+    """Every code times scales of 24 bits, most of them such that the product lies next to the
+    middle of two bf16 values (m / 8 times the scale, m odd, is one, or a step of fp32 beside
+    it): rounded to fp32 first, it would come to lie on it. A product of 4 and 24 bits is exact in
+    float64."""
+    rng = np.random.default_rng(9)
+    values = O.E4M3_TABLE[np.arange(256)]
+    fin = np.isfinite(values)
+    scales = [np.float32(rng.random() + 0.5) for _ in range(20)] + [np.float32(2.0 ** -100 / 3)]
+    for m in (9, 11, 13, 15):
+        for k in rng.integers(0, 128, 10):
+            s = np.float32((1 + (2 * k + 1) * 2.0 ** -8) * 8 / m)
+            scales += [s, np.nextafter(s, np.float32(9)), np.nextafter(s, np.float32(0))]
+    cache = torch.from_numpy(np.resize(np.arange(256, dtype=np.uint8), (1, 512))).cuda()
+    slot, ws, twice = i32([0]), small_ws(), 0
+    out = torch.empty((1, 512), dtype=torch.bfloat16, device="cuda")
+    for s in scales:
+        dsa.kv_read(dsa.config(kv_fmt=dsa.KV_FP8_E4M3, kv_scale=float(s)), cache, slot, out, ws)
+        got = out[0, :256].double().cpu().numpy()
+        assert np.isnan(got[~fin]).all()
+        exact = values[fin] * float(s)
+        mant, e = np.frexp(exact)
+        want = np.ldexp(np.rint(mant * 256), e - 8)  # 8 bits, ties to even
+        assert np.array_equal(got[fin], want), s
+        twice += int((want != O.bf16_to_f64(O.f32_to_bf16_rne(exact.astype(np.float32)))).sum())
+    assert twice  # the cases are such
     assert dsa.read_device_status(ws)[0] == 0

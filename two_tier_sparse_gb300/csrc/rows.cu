@@ -49,6 +49,17 @@ __device__ __forceinline__ float quotient(float x, float s, float y) {
   return fabsf(q0) <= 1000.f && q0 != 0.f ? q2 : q0;
 }
 
+// x s for a further rounding to bf16: cut off to fp32, its last bit set where something was cut
+// (rounding to odd: Boldo and Melquiond, "Emulation of FMA and correctly rounded sums: proved
+// algorithms using rounding to odd", 2008). A product rounded to nearest here could come to lie
+// halfway between two bf16 values when it does not. The remainder is exact down to products of
+// 2^-122 (four bits of a code and 24 of a scale).
+__device__ __forceinline__ float product_odd(float x, float s) {
+  const float p = __fmul_rz(x, s);
+  const bool cut = fmaf(x, s, -p) != 0.f;
+  return __uint_as_float(__float_as_uint(p) | (cut ? 1u : 0u));
+}
+
 template <int FMT>
 __global__ void __launch_bounds__(256) kv_write_kernel(RowsArgs a) {
   griddep_wait();
@@ -131,7 +142,8 @@ __global__ void __launch_bounds__(256) kv_read_kernel(RowsArgs a) {
           const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
               static_cast<__nv_fp8x2_storage_t>((cw[i >> 1] >> (16 * (i & 1))) & 0xFFFF), __NV_E4M3);
           const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hr));
-          const __nv_bfloat162 p = __floats2bfloat162_rn(f.x * a.kv_scale, f.y * a.kv_scale);
+          const __nv_bfloat162 p = __floats2bfloat162_rn(product_odd(f.x, a.kv_scale),
+                                                         product_odd(f.y, a.kv_scale));
           w[i] = *reinterpret_cast<const uint32_t*>(&p);
         }
         x[h] = make_uint4(w[0], w[1], w[2], w[3]);
