@@ -378,3 +378,44 @@ def test_append_to_a_four_bit_cache(ratio, page_rows):
                              "mxfp4")
         v = O.latent_values(got[n - 1], "mxfp4")
         assert np.all((v == lo) | (v == hi)), b
+
+
+@pytest.mark.parametrize("B", [1, 3, 20, 40, 77, 160])  # eight, four and two CTAs a sequence, one
+@pytest.mark.parametrize("place", ["latent", "window"])
+def test_a_nan_row_makes_every_head_of_its_sequence_nan(B, place):
+    """Every score against a NaN row is NaN, and so are each head's sum, its output in every
+    dim and its log-sum-exp; the other sequences are as without it."""
+    c = Case([300 + b % 3 for b in range(B)], 200, 64, seed=B)
+    want = c.run()
+    hit = sorted({0, B // 2, B - 1})
+    for b in hit:
+        if place == "latent":
+            c.latents[b, c.ids[b, (7 * b + 150) % 200], 256 + b % 16] = 255
+        else:
+            c.swa[b, (5 * b + 3) % 64, 256 + b % 16] = 255
+    c.dlat = dev(c.latents)
+    out, lse = c.run()
+    got = out.view(torch.bfloat16)
+    keep = [b for b in range(B) if b not in hit]
+    assert bool(got[hit].isnan().all()) and bool(lse[hit].isnan().all())
+    assert torch.equal(out[keep], want[0][keep]) and torch.equal(lse[keep], want[1][keep])
+    assert not bool(want[0].view(torch.bfloat16).isnan().any()) and bool(want[1].isfinite().all())
+    assert dsa.read_device_status(c.ws)[0] == 0
+
+
+@pytest.mark.parametrize("B", [1, 20, 77, 160])
+def test_a_head_of_nan_stays_with_itself(B):
+    c = Case([300] * B, 200, 64, seed=B)
+    want = c.run()
+    hit = sorted({0, B - 1})
+    for b in hit:
+        c.q[b, 5, 17], c.q[b, 40, 0] = 0x7FC0, 0x7F80  # NaN, and an infinite element
+    out, lse = c.run()
+    got = out.view(torch.bfloat16)
+    rest = [h for h in range(64) if h not in (5, 40)]
+    for b in range(B):
+        if b in hit:
+            assert bool(got[b, [5, 40]].isnan().all()) and bool(lse[b, [5, 40]].isnan().all())
+        else:
+            assert torch.equal(out[b], want[0][b])
+        assert torch.equal(out[b, rest], want[0][b, rest]) and torch.equal(lse[b, rest], want[1][b, rest])
