@@ -1,5 +1,7 @@
 """Edges of the serving calls on the GPU: page ids that are no pages, frequencies and positions
-of any size, cache elements that are no numbers. Tolerances as in test_gpu_serving.py, where nothing else is said."""
+of any size, cache elements that are no numbers, the binding without its compiled part, decode
+steps right behind what writes their inputs. Tolerances as in test_gpu_serving.py, where
+nothing else is said."""
 from fractions import Fraction
 
 import numpy as np
@@ -225,3 +227,81 @@ def test_e4m3_rows_read_are_rounded_once():
         twice += int((want != O.bf16_to_f64(O.f32_to_bf16_rne(exact.astype(np.float32)))).sum())
     assert twice  # the cases are such
     assert dsa.read_device_status(ws)[0] == 0
+
+
+KV_FORMATS = [dsa.KV_BF16, dsa.KV_FP8_E4M3, dsa.KV_MXFP4]
+
+
+class LoneStep:
+    """A decode step of one sequence over `n` latents of zeros and a window of two rows,
+    contiguous caches; more blocks than the candidate stage keeps, so it scans them."""
+
+    def __init__(self, fmt, n):
+        self.cfg = dsa.config(kv_fmt=fmt, window=2, k_tokens=8, k_blocks=4)
+        self.ws = dsa.workspace(self.cfg, 1, 256)
+        row, dt = {dsa.KV_BF16: (512, torch.bfloat16), dsa.KV_FP8_E4M3: (512, torch.uint8),
+                   dsa.KV_MXFP4: (272, torch.uint8)}[fmt]
+        z = dict(device="cuda")
+        self.swa = torch.zeros((1, 2, row), dtype=dt, **z)
+        self.lat = torch.zeros((1, 256, row), dtype=dt, **z)
+        self.keys = dsa.Keys("bf16", torch.zeros((1, 256, 128), dtype=torch.bfloat16, **z))
+        self.pooled = dsa.Keys("bf16", torch.zeros((1, 32, 128), dtype=torch.bfloat16, **z))
+        self.q_idx = torch.zeros((1, 16, 128), dtype=torch.bfloat16, **z)
+        self.w = torch.zeros((1, 16), **z)
+        self.n = i32([n])
+
+    def __call__(self, q, swa_len, out, update_pool):
+        dsa.decode_step(self.cfg, q, self.q_idx, self.w, self.keys, self.pooled, self.lat, self.n,
+                        256, self.swa, swa_len, out, self.ws, update_pool=update_pool)
+
+
+def outputs(n):
+    return [torch.empty((1, 64, 512), dtype=torch.bfloat16, device="cuda") for _ in range(n)]
+
+
+@pytest.mark.parametrize("update_pool", [False, True])
+@pytest.mark.parametrize("n", [0, 256])
+@pytest.mark.parametrize("fmt", KV_FORMATS)
+def test_a_row_written_right_before_a_decode_step_is_read(fmt, n, update_pool):
+    """kv_write of the one window row -> decode_step with nothing between, many times over. The query
+    is zero, so the output is the row over the number of rows (itself and 8 latents of
+    zeros): within 2^-7 of that, where neighbouring calls' rows differ by a factor of 2."""
+    step = LoneStep(fmt, n)
+    q, one, zero = torch.zeros((1, 64, 512), dtype=torch.bfloat16, device="cuda"), i32([1]), i32([0])
+    rows = [torch.full((1, 512), 2.0 ** (i % 8), dtype=torch.bfloat16, device="cuda") for i in range(60)]
+    outs = outputs(60)
+    torch.cuda.synchronize()
+    for r, o in zip(rows, outs):
+        dsa.kv_write(step.cfg, r, zero, step.swa, step.ws)
+        step(q, one, o, update_pool)
+    torch.cuda.synchronize()
+    share = 1.0 if n == 0 else 1.0 / 9
+    for r, o in zip(rows, outs):
+        want = float(r[0, 0]) * share
+        assert bool(((o.float() - want).abs() <= 2.0 ** -7 * want).all())
+    assert dsa.read_device_status(step.ws)[0] == 0
+
+
+@pytest.mark.parametrize("update_pool", [False, True])
+@pytest.mark.parametrize("fmt", KV_FORMATS)
+def test_queries_normed_right_before_a_decode_step_are_read(fmt, update_pool):
+    """norm_rope of the query in place -> decode_step with nothing between. The window holds a row
+    of ones and its negative; a normed query of +-1 has scores +-22.6, so the output is the
+    row of its sign (e^-45 of the other), while the query before its norm weighs both alike."""
+    step = LoneStep(fmt, 0)
+    both = torch.ones((2, 512), dtype=torch.bfloat16, device="cuda")
+    both[1] = -1
+    dsa.kv_write(step.cfg, both, i32([0, 1]), step.swa, step.ws)
+    two = i32([2])
+    signs = np.where(np.random.default_rng(6).random(60) < 0.5, -1.0, 1.0)
+    qs = [torch.full((1, 64, 512), s * 2.0 ** -20, dtype=torch.bfloat16, device="cuda") for s in signs]
+    sets = [dsa.HeadSet([dsa.Heads(q, eps=0.0)]) for q in qs]
+    outs = outputs(60)
+    torch.cuda.synchronize()
+    for q, h, o in zip(qs, sets, outs):
+        dsa.norm_rope(None, h)
+        step(q, two, o, update_pool)
+    torch.cuda.synchronize()
+    for s, q, o in zip(signs, qs, outs):
+        assert bool((q == s).all()) and bool((o == s).all())
+    assert dsa.read_device_status(step.ws)[0] == 0
