@@ -578,6 +578,8 @@ dsa_status_t dsa_norm_rope(int n, const int32_t* n_valid, const int32_t* positio
  *   slots:   device int32 [n] (a plan's latent_slots or window_slots)
  *   cache:   n_rows rows of the format (n_pages * page_rows for a pool,
  *            B * window for the window rows); n_rows < 2^31
+ * The workspace may be of any size that dsa_workspace_size gives: its status word alone is
+ * used here and in dsa_kv_read, however many rows there are.
  */
 dsa_status_t dsa_kv_write(const dsa_config_t* cfg, int n, const int32_t* n_valid, const void* rows,
                           int64_t row_stride, const int32_t* slots, void* cache, int64_t n_rows,
@@ -586,8 +588,7 @@ dsa_status_t dsa_kv_write(const dsa_config_t* cfg, int n, const int32_t* n_valid
 /*
  * Rows out of a cache: row slots[r] of `cache` as bf16 to row r of `rows`, code
  * times scale (exact for MXFP4 scales up to 2^125; rounded once for E4M3, products
- * of at least 2^-122). Rows
- * with a negative slot are left as they were. A cache of any format so serves
+ * of at least 2^-122). Rows with a negative slot are left as they were. A cache of any format so serves
  * the calls that read bf16 rows (a sequence's latents for dsa_sparse_attn_prefill).
  */
 dsa_status_t dsa_kv_read(const dsa_config_t* cfg, int n, const int32_t* n_valid, const void* cache,

@@ -470,7 +470,8 @@ class StepPlan:
 
 def plan_step(cfg, n_tokens, n_new, pool: PagePool, plan: StepPlan, ws, stream=None):
     """Block table and slot maps of a step (dsa_plan_step): n_tokens [B] lengths
-    before the step, n_new [B] tokens added (negative: the request ends)."""
+    before the step, n_new [B] tokens added (negative: the request ends). ws: any workspace,
+    workspace(cfg, 1, 0) will do."""
     if stream is None:  # the plain case (None: any other)
         code = (_calls or _load_calls()).plan(cfg, n_tokens, n_new, pool._key, plan._key, ws)
         if code is not None:
@@ -623,7 +624,7 @@ def _rows_call(name, cfg, rows, slots, cache, ws, n_valid, stream):
 def kv_write(cfg, rows, slots, cache, ws, n_valid=None, stream=None):
     """bf16 rows [n, 512] into a cache of cfg.kv_fmt (dsa_kv_write): row r becomes cache
     row slots[r], negative slots skip; cache: [..., row] contiguous (a pool of pages, or
-    the window rows)."""
+    the window rows). ws: any workspace, workspace(cfg, 1, 0) will do."""
     if stream is None:
         code = (_calls or _load_calls()).rows(True, cfg, rows, slots, cache, ws, n_valid)
         if code is not None:
@@ -633,7 +634,7 @@ def kv_write(cfg, rows, slots, cache, ws, n_valid=None, stream=None):
 
 def kv_read(cfg, cache, slots, rows, ws, n_valid=None, stream=None):
     """Rows slots[r] of a cache back as bf16 rows [n, 512] (dsa_kv_read); rows with a
-    negative slot are left as they were."""
+    negative slot are left as they were. ws: as for kv_write."""
     if stream is None:
         code = (_calls or _load_calls()).rows(False, cfg, rows, slots, cache, ws, n_valid)
         if code is not None:
