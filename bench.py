@@ -403,7 +403,8 @@ def run_ours(args):
     kv_fmt = spec.get("kv_fmt", "bf16")
     inp = synth.decode_inputs([T] * B, ratio, fmt, shard_seed(spec["seed"], rank), kv_fmt=kv_fmt)
     gen_s = time.time() - t0
-    cfg = dsa.config(ratio=ratio, kv_fmt=dsa.KV_FP8_E4M3 if kv_fmt == "fp8" else dsa.KV_BF16,
+    cfg = dsa.config(ratio=ratio, kv_fmt={"bf16": dsa.KV_BF16, "fp8": dsa.KV_FP8_E4M3,
+                                          "mxfp4": dsa.KV_MXFP4}[kv_fmt],
                      kv_scale=inp.kv_scale)
     cap = inp.cap
     L = int(inp.n_latents.max())
@@ -642,8 +643,8 @@ def run_ours(args):
     hbm_peak, _, peak_kind = measured_peaks()
     achieved = bytes_per_launch / (scan_avg_ms * 1e-3) / 1e9
     # whole-step algorithmic bytes (keys scanned + latent rows gathered + window + q/out;
-    # a latent or window row is 1024 bytes in bf16, 512 in fp8)
-    kv_row = 512 if kv_fmt == "fp8" else 1024
+    # a latent or window row is 1024 bytes in bf16, 512 in fp8, 272 in mxfp4)
+    kv_row = {"bf16": 1024, "fp8": 512, "mxfp4": dsa.KV_MXFP4_ROW}[kv_fmt]
     step_bytes = B * (blk_rows * row_bytes + tok_rows * row_bytes + 512 * kv_row + 128 * kv_row
                       + 64 * 512 * 2 * 2 + 16 * 128 * 2)
     traffic = None

@@ -177,7 +177,7 @@ class DecodeInputs:
     window: int = WINDOW
     meta: dict = field(default_factory=dict)
     # "fp8": latents and window rows are E4M3 codes (uint8 [.., 512]) standing
-    # for code * kv_scale
+    # for code * kv_scale; "mxfp4": 4-bit rows (uint8 [.., 272]: codes, then scales)
     kv_fmt: str = "bf16"
     kv_scale: float = 1.0
 
@@ -202,7 +202,9 @@ def decode_inputs(T, ratio: int, key_fmt: str, seed: int, window: int = WINDOW,
     poison_tail fills rows past each sequence's end with +inf (bf16) or the
     largest MXFP8 or MXFP4 value, so a kernel that reads them gives a visibly wrong result.
     kv_fmt "fp8": latents and window rows are the E4M3 codes of the same
-    N(0,1)/sqrt(512) values divided by kv_scale (rows past the end: 448).
+    N(0,1)/sqrt(512) values divided by kv_scale (rows past the end: 448);
+    "mxfp4": the MXFP4 rows of those values, 256 bytes of codes and 16 scales each (rows
+    past the end: NaN scales).
     """
     T = np.asarray(T, np.int64).reshape(-1)
     B = int(T.shape[0])
@@ -215,11 +217,12 @@ def decode_inputs(T, ratio: int, key_fmt: str, seed: int, window: int = WINDOW,
     q = np.empty((B, N_HEADS, LATENT_DIM), np.uint16)
     q_idx = np.empty((B, N_IDX_HEADS, IDX_DIM), np.uint16)
     w = np.empty((B, N_IDX_HEADS), np.float32)
-    if kv_fmt not in ("bf16", "fp8"):
+    if kv_fmt not in ("bf16", "fp8", "mxfp4"):
         raise ValueError(kv_fmt)
-    fp8 = kv_fmt == "fp8"
-    lat = np.empty((B, cap, LATENT_DIM), np.uint8 if fp8 else np.uint16)
-    swa = np.zeros((B, window, LATENT_DIM), np.uint8 if fp8 else np.uint16)
+    kv_row = {"mxfp4": LATENT_DIM // 2 + LATENT_DIM // 32}.get(kv_fmt, LATENT_DIM)
+    kv_type = np.uint16 if kv_fmt == "bf16" else np.uint8
+    lat = np.empty((B, cap, kv_row), kv_type)
+    swa = np.zeros((B, window, kv_row), kv_type)
     swa_len = np.minimum(T, window).astype(np.int32)
     if key_fmt == "bf16":
         kdata = np.empty((B, cap, IDX_DIM), np.uint16)
@@ -238,7 +241,11 @@ def decode_inputs(T, ratio: int, key_fmt: str, seed: int, window: int = WINDOW,
         normal_bf16(seed, TAG_QIDX, off, N_IDX_HEADS * IDX_DIM, s128, out=q_idx[b].reshape(-1))
         w[b] = uniform_f32(seed, TAG_W, off, N_IDX_HEADS)
         n_sw = int(swa_len[b])
-        if fp8:
+        if kv_fmt == "mxfp4":
+            for rows, tag, n in ((lat[b], TAG_LAT, cap), (swa[b], TAG_SWA, n_sw)):
+                codes, scales = normal_mxfp4(seed, tag, b << 31, n, LATENT_DIM, s512)
+                rows[:n, :LATENT_DIM // 2], rows[:n, LATENT_DIM // 2:] = codes, scales
+        elif kv_fmt == "fp8":
             normal_e4m3(seed, TAG_LAT, off, cap * LATENT_DIM, s512, kv_scale,
                         out=lat[b].reshape(-1))
             if n_sw:
@@ -259,7 +266,7 @@ def decode_inputs(T, ratio: int, key_fmt: str, seed: int, window: int = WINDOW,
                          scales=kscales[b])
         if poison_tail:
             n = int(n_lat[b])
-            lat[b, n:] = BF16_POS_INF if kv_fmt == "bf16" else 0x7E
+            lat[b, n:] = {"bf16": BF16_POS_INF, "fp8": 0x7E, "mxfp4": 0xFF}[kv_fmt]
             if key_fmt == "bf16":
                 kdata[b, n:] = BF16_POS_INF
             elif key_fmt == "mxfp8":
@@ -445,6 +452,10 @@ WORKLOADS = {
     # configurations, --kv-cache-dtype fp8).
     "decode_b64_t131072_r1_mxfp8_fp8kv": dict(kind="decode", B=64, T=131072, ratio=1,
                                               key_fmt="mxfp8", seed=2, kv_fmt="fp8"),
+    # The same batch with a 4-bit KV cache (latents and window rows as MXFP4;
+    # miles.radixark.com "DeepSeek-V4.1 Flash", latents "trained to be stored in FP4").
+    "decode_b64_t131072_r1_mxfp8_mxfp4kv": dict(kind="decode", B=64, T=131072, ratio=1,
+                                                key_fmt="mxfp8", seed=2, kv_fmt="mxfp4"),
     # Multi-query decode: the 64 x 131072 batch with 5 queries a sequence (a
     # DSpark block of draft tokens verified in one pass).
     "decode_mq5_b64_t131072_r1_mxfp8": dict(kind="multi", B=64, n_q=5, T=131072, ratio=1,

@@ -88,3 +88,15 @@ def test_prefill_workload_full_size():
             check_ids(tok[i], r["token_ids"], lambda j: pos[j], cfg.k_tokens, f"q{i}")
         r2 = O.prefill_query(oc, pf, i, kv, pooled, token_ids=tok[i])
         check_out(out[i], lse[i], r2["out"], r2["lse"], f"q{i}")
+
+
+def test_decode_workload_full_size_over_a_four_bit_cache():
+    inp = synth.workload_inputs("decode_b64_t131072_r1_mxfp8_mxfp4kv")
+    cfg = dsa.config(kv_fmt=dsa.KV_MXFP4)
+    d = DecodeOnDevice(inp, cfg)
+    d.pool()
+    outs = run_step(d, cfg, update_pool=True)
+    code, info = d.status()
+    assert code == 0, hex(info)
+    check_all_sequences(inp, cfg, outs)
+    check_step(inp, cfg, outs, [0, 31, 63])

@@ -81,3 +81,17 @@ def test_fp8_cache_codes_match_the_oracle_encoder():
     inp = synth.decode_inputs([300, 20], 1, "mxfp8", seed=6, kv_fmt="fp8")
     assert inp.latents.dtype == np.uint8 and inp.swa.dtype == np.uint8
     assert (inp.latents[1, 20:] == 0x7E).all()  # the poisoned tail: 448
+
+
+def test_four_bit_cache_rows_match_the_oracle_encoder():
+    """synth's 4-bit cache rows (its own C conversion) are the oracle's MXFP4 rows of the same fp32
+    normals; rows past a sequence's end have NaN scales."""
+    inp = synth.decode_inputs([300, 20], 1, "mxfp8", seed=6, kv_fmt="mxfp4")
+    s = 1 / np.sqrt(512)
+    for b, n in ((0, 300), (1, 20)):
+        v = synth.normal_f32(6, synth.TAG_LAT, b << 40, n * 512, s).reshape(n, 512)
+        assert np.array_equal(inp.latents[b, :n], O.latent_rows_mxfp4(v))
+        w = min(n, 128)
+        v = synth.normal_f32(6, synth.TAG_SWA, b << 40, w * 512, s).reshape(w, 512)
+        assert np.array_equal(inp.swa[b, :w], O.latent_rows_mxfp4(v))
+        assert (inp.latents[b, n:, 256:] == 255).all()
