@@ -514,8 +514,9 @@ typedef enum { DSA_DT_BF16 = 0, DSA_DT_F16 = 1, DSA_DT_F32 = 2 } dsa_dtype_t;
  * x_head_stride + 0 .. dim - 1], and goes to out by out's strides. Strides count
  * elements and, like the base pointers, are multiples of 16 bytes; that of a single
  * token or head is not used. out's heads do not overlap (DSA_ERR_INVALID_ARG). out may be
- * x with the same strides (in place); they must not overlap otherwise, nor may two groups'
- * outputs. */
+ * x with the same strides (in place); they must not overlap otherwise. Nor may a group's out
+ * overlap another's x or out, since nothing orders the groups of a call (that is refused
+ * where two of them start at one address); groups may read the same x. */
 typedef struct {
   const void* x;
   void* out;

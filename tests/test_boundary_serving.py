@@ -267,3 +267,23 @@ def test_rotations_that_start_past_the_head_are_refused(lib, dim, rope_dim):
                         out_token_stride=2 * dim, out_head_stride=dim, weight=A, eps=1e-6, norm=1,
                         rope_start=start)
         assert lib.dsa_norm_rope(4, None, A, 0, ctypes.byref(h), 1, ctypes.byref(rope), None) == 1, start
+
+
+def test_groups_that_write_what_another_reads_or_writes_are_refused(lib):
+    """One launch runs the groups in no order: a group's output that is another's input (that
+    group in place, say) or output is refused where they start at one address. Inputs may be shared."""
+    def call(*groups, n=4):
+        arr = (dsa._HeadsC * len(groups))()
+        for h, (x, out, heads) in zip(arr, groups):
+            h.x, h.out, h.heads, h.dim, h.rope_start, h.norm = x, out, heads, 64, -1, 1
+            h.x_token_stride = h.out_token_stride = 128
+            h.x_head_stride = h.out_head_stride = 64
+        return lib.dsa_norm_rope(n, None, None, 0, arr, len(groups), None, None)
+    x, y, z = A, 2 * A, 3 * A
+    assert call((x, y, 2), (z, y, 2)) == 1        # two outputs
+    assert call((x, x, 2), (x, y, 2)) == 1        # in place, and read by another
+    assert call((x, y, 2), (x, x, 2)) == 1
+    assert call((x, y, 2), (y, z, 1)) == 1        # one's output, another's input
+    assert call((y, z, 1), (5 * A, 6 * A, 1), (x, y, 2)) == 1
+    assert call((x, x, 2), (x, y, 2), n=0) == 0   # nothing is read or written
+    assert call((x, x, 0), (x, y, 0)) == 0

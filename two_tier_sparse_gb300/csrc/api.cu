@@ -1130,6 +1130,11 @@ dsa_status_t dsa_norm_rope(int n, const int32_t* n_valid, const int32_t* positio
     }
     if (heads_overlap(h.dim, h.heads, oh, n, ot)) return DSA_ERR_INVALID_ARG;
     if (h.x == h.out && (xt != ot || xh != oh)) return DSA_ERR_INVALID_ARG;
+    for (int k = 0; k < used; ++k) {  // (nothing orders two groups)
+      if (h.out == a.seg[k].out || h.out == a.seg[k].x || h.x == a.seg[k].out) {
+        return DSA_ERR_INVALID_ARG;
+      }
+    }
     NormRopeSeg& sg = a.seg[used++];
     sg.x = h.x;
     sg.out = h.out;

@@ -3,7 +3,8 @@
 // and [256 + 8 l, 256 + 8 l + 8), so every access of a warp is contiguous and
 // a 32-element scale group is four neighbouring lanes. Bound by memory: 65536 rows to slots
 // in any order take 15.5 us as MXFP4 (5.5 TB/s), 20.6 as E4M3 (4.9, its conversion in part), 22.3 as
-// bf16 (6.0); out of the cache 16.0, 17.7 and 22.5. All 64 warps of an SM have a row on its way:
+// bf16 (6.0); out of the cache 16.0, 17.7 and 22.5. All 64 warps of an SM have a row on its way (48 to
+// E4M3, whose quotients take 35 registers):
 // with half of them MXFP4 takes 19.9 us.
 #include <algorithm>
 
