@@ -265,11 +265,11 @@ __global__ void __launch_bounds__(32 * kWarps, NV == 1 ? 3 : NV == 2 ? 2 : 1)
     }
     if (sg.rope && table_of != tok) {
       table_of = tok;
-      const int64_t pos = a.positions[tok];
+      const uint64_t pos = static_cast<uint64_t>(int64_t{a.positions[tok]});
       __syncwarp();
       for (int k = lane; k < pairs; k += 32) {
         const double f = a.inv_freq[k];
-        const int64_t turn = pos * static_cast<int64_t>(turn_bits(f, a.inv_2pi));
+        const int64_t turn = static_cast<int64_t>(pos * turn_bits(f, a.inv_2pi));  // (modulo 2^64)
         float sn, cs;
         sincospif(angle_exists(f) ? static_cast<float>(turn) * 0x1p-63f  // half turns, from -1 to 1
                                   : __int_as_float(0x7FC00000),          // (NaN)
