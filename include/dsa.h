@@ -441,7 +441,10 @@ dsa_status_t dsa_topk_noalloc(const dsa_config_t* cfg, const void* q_idx, const 
  * keys it takes, and the cache rows it reads. A decode loop calls
  *     dsa_plan_step -> dsa_norm_rope -> dsa_compress_append and dsa_kv_write
  *     -> dsa_decode_step
- * on one stream, all from device memory, and captures into a CUDA graph.
+ * on one stream, all from device memory, and captures into a CUDA graph. dsa_norm_rope and
+ * dsa_kv_write do nothing in a step that the plan refuses (it counts no token and gives no slot).
+ * dsa_compress_append goes by the token counts that it is given, and would write a complete group's
+ * latent again: give it 0 for a request without a new token (where cu_new does not grow).
  */
 
 /* A pool of pages that requests share, and its free pages. */

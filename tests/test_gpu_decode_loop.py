@@ -229,3 +229,63 @@ def test_a_decode_loop_over_a_four_bit_cache(captured):
     held = sum(-(-n // 64) for n in s.n.tolist())
     head, tail = s.pool.ring_state.tolist()
     assert tail - head == 40 - held
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_a_refused_step_of_the_loop_leaves_the_caches(captured):
+    """Too few free pages for a step: the plan refuses it, and the calls behind it, whose counts and
+    slots are the plan's, write no cache row either (the append takes 0 tokens for requests that got
+    none). With the pages there, the same step is the one that was never refused."""
+    B, R = 3, 64
+    runs = []
+    for refuse in (True, False):
+        s = Server(B, R, 3, 12, 200, 16, 8)
+        g = torch.Generator(device="cuda").manual_seed(5)
+
+        def projections(total):
+            return [torch.randn(sh, generator=g, device="cuda").bfloat16()
+                    for sh in ((total, 64, 512), (total, 512), (total, 16, 128), (total, 128))]
+
+        def decode():
+            s.make()
+            grown = s.plan.n_tokens * (s.plan.cu_new[1:] > s.plan.cu_new[:-1])
+            dsa.compress_append(s.cfg, grown, s.kv[:B], gate, dsa.Keys("bf16", s.k_idx[:B]), s.latents,
+                                s.keys, s.pooled, s.cap, s.ws)
+            dsa.decode_step(s.cfg, s.q[:B], s.q_idx[:B], s.w, s.keys, s.pooled, s.latents,
+                            s.plan.n_latents, s.cap, s.swa, s.plan.swa_len, s.out, s.ws, lse=s.lse,
+                            token_ids=s.ids)
+        gate = torch.zeros((B, 1), device="cuda")
+        s.take(projections(64 + 10 + 100))
+        s.new.copy_(i32([64, 10, 100]))  # the first request's page is full
+        s.prompts()
+        s.new.copy_(i32([1] * B))
+        x = projections(B)
+        s.take(x)
+        step = decode
+        if captured:
+            decode()  # (sets limits; taken back below)
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                decode()
+            step = graph.replay
+            s.n.sub_(1)
+            s.pool.ring_state[0] -= 1
+            s.take(x)
+        if refuse:
+            state = s.pool.ring_state.clone()
+            s.pool.ring_state[0] = state[1]  # no page is free
+            caches = (s.latents, s.swa, s.keys.data, s.pooled.data, s.pool.table, s.n)
+            before = [t.clone() for t in caches]
+            step()
+            assert dsa.read_device_status(s.ws)[0] == 6
+            for t, b in zip(caches, before):
+                assert torch.equal(t, b)
+            s.pool.ring_state.copy_(state)
+            s.take(x)
+        step()
+        assert dsa.read_device_status(s.ws)[0] == 0
+        assert s.n.tolist() == [65, 11, 101]
+        runs.append([t.clone() for t in (s.out, s.lse, s.ids, s.latents, s.swa, s.pooled.data)])
+    for a, b in zip(*runs):
+        assert torch.equal(a, b)
