@@ -581,7 +581,8 @@ dsa_status_t dsa_norm_rope(int n, const int32_t* n_valid, const int32_t* positio
  *   n_valid: as in dsa_norm_rope
  *   slots:   device int32 [n] (a plan's latent_slots or window_slots)
  *   cache:   n_rows rows of the format (n_pages * page_rows for a pool,
- *            B * window for the window rows); n_rows < 2^31
+ *            B * window for the window rows); n_rows < 2^31; `rows` does not overlap it
+ *            (here and in dsa_kv_read)
  * The workspace may be of any size that dsa_workspace_size gives: its status word alone is
  * used here and in dsa_kv_read, however many rows there are.
  */
