@@ -115,7 +115,8 @@ typedef struct {
  * f16 operands; the probabilities are f16 too (bf16 with bf16 rows). The dsa_full_attn
  * calls multiply the codes as they are: the query enters as the sum of two E4M3 values a
  * element, exact down to 2^-10 of its head's largest element and within 2^-18 of that below, and so do
- * the probabilities, rounded as to bf16 down to 2^-5 of the largest and to 2^-15 of it below.
+ * the probabilities, rounded as to bf16 but for small ones, of which the roundings together
+ * change the sum by at most 2^-8 + 2^-9 of it, however many rows there are.
  * Latents "trained to be stored in FP4" (miles.radixark.com "DeepSeek-V4.1
  * Flash") are read as OCP MXFP4, the format of the 4-bit index keys. 4-bit
  * rows are taken by the calls above and by dsa_compress_append; prefill and

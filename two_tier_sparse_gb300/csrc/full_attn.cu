@@ -35,9 +35,16 @@
 // E4M3 codes are MMA operands as they are (K = 32 a step), so Q and P are E4M3 too, as sums of two:
 // a bf16 has 8 significant bits and E4M3 4, so x = hi + lo with hi = RN(x) and lo = RN(x - hi)
 // is exact down to E4M3's smallest step. Q, scaled by a power of two a head to at most 448, is exact for
-// elements down to 2^-10 of the head's largest and within 2^-18 of that below. P, between
-// 0 and 256 with its largest at least 32, is rounded to 8 bits (as bf16 would) or 2^-10, 2^-15 of
-// its largest. Both halves are products of their own with the same accumulators, so the MMAs cost
+// elements down to 2^-10 of the head's largest and within 2^-18 of that below. P is rounded to 8
+// bits (as bf16 would) or by 2^-10, whichever is more. The second is a fixed step, and a long tail of small
+// probabilities would get lost in it if P were in units of the largest so far. So the units follow
+// the tiles, down too: of each tile the largest P is at least 2^5, whose sum the 128 roundings change by at
+// most 2^-8, or the sum before it is at least 64 times the run's tiles of the query, whose sum all
+// such tiles together change by at most 2^-9. Moving the unit scales the output in tensor memory; the
+// sum soon suffices where no few rows have most of the weight (64 x 8192: 77 us with units of the largest
+// and with these at scores spread by 0.6 nats, 79 -> 83 at 1.3, 83 -> 86 at 6; with units of the largest
+// and a first row of half the weight, 0.03 of the sum was lost over 16384 rows, 0.38 over 131072).
+// Both halves are products of their own with the same accumulators, so the MMAs cost
 // what those of bf16 rows do (twice the products at twice the K), and rows are half the
 // bytes. (Converted to f16 by loader warps 64 rows took 3.3 us.)
 #include <algorithm>
@@ -68,7 +75,7 @@ constexpr int kSlotBytes = 64 * 1024;
 constexpr int kStage = kKV + kSlots * kSlotBytes;  // an output warp's 64 bytes of 32 heads
 constexpr int kStageBytes = 32 * 64;
 constexpr int kMisc = kStage + 4 * kStageBytes;
-constexpr int kMiscBytes = 5120;
+constexpr int kMiscBytes = 6144;
 constexpr int kSmemBytes = kMisc + kMiscBytes + 1024;  // + alignment slack of the base
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 constexpr int kTmemCols = 512;
@@ -89,8 +96,12 @@ struct Shape {
   // Tiles by which the longest run of whole queries may exceed the even split's runs: kFew while
   // those are the shortest there are (few parts then: 16 sequences of 640 bf16 rows 14.4 us split, 22.0 whole).
   static constexpr int kMore = kF8 ? 7 : kTma ? 12 : 8, kFew = kF8 ? 3 : 5;
-  // P = 2^(z - m + kUp) with m the running maximum, moved when it is 2^kSlack behind: P <= 2^8
-  static constexpr float kUp = kF8 ? 5.f : 0.f, kSlack = kF8 ? 3.f : 8.f;
+  // P = 2^(z - m + kUp), m the reference: a tile's largest z, moved up when another tile's is more
+  // than kSlack above it (E4M3: P <= 2^8.8 < 448; else 2^8) ...
+  static constexpr float kUp = kF8 ? 6.f : 0.f, kSlack = kF8 ? 2.8f : 8.f;
+  // ... and, over E4M3 rows, down (by 2^kFar at most) when it is more than kDrop below it and the
+  // sum so far less than kNeed times the run's tiles of the query.
+  static constexpr float kDrop = 1.f, kNeed = 64.f, kFar = 24.f;
   static constexpr int kLoadWarps = kTma ? 1 : 8;
   static constexpr int kMmaWarp = kLoadWarp0 + kLoadWarps;
   static constexpr int kPvWarp = kMmaWarp + 1;
@@ -180,6 +191,7 @@ struct Misc {
   int2 warp_sum[8];        // of the tiles: the sum and the largest of a warp's queries
   int2 bound[kFullMaxCtas + 1];  // where runs of whole queries begin: the tile and its query
   float mx[2][2][kHeads];  // a tile's largest score of each head in its two halves
+  float sum[2][2][kHeads];  // (E4M3) the two halves' sums before the tile
   // of a query, by its parity: the output warps may be one behind
   float m_of[2][kHeads], l_of[2][kHeads];
   float wgt[2][kHeads];    // what a head's O is scaled by
@@ -812,6 +824,7 @@ __global__ void __launch_bounds__(Shape<FMT>::kThreads, 1)
         auto wait_pv = [&](int t) {
           if (ok) ok = wait_bar(&misc->p_empty, static_cast<uint32_t>(t & 1), misc, a.status);
         };
+        const float need = Sh::kNeed * static_cast<float>(p.take);
         for (int j = 0; j < p.take; ++j, ++tt) {
           const int sb = tt & 1, slot = tt % kSlots;
           float z[kHalf];
@@ -845,19 +858,28 @@ __global__ void __launch_bounds__(Shape<FMT>::kThreads, 1)
           }
           // The buffer of tile tt - 2 is free: its readers have passed tile tt - 1's barrier.
           misc->mx[sb][half][h] = mt;
-          // If any head's maximum moved by more than 2^kSlack (or there is none yet), both halves
-          // take the larger one.
-          if (named_sync_or(kMathBar, 128, j == 0 || mt > m_run + Sh::kSlack)) {
+          if (kF8) misc->sum[sb][half][h] = l_run;
+          // If any head's reference may have to move (or there is none yet), both halves see
+          // what is to be done with the larger maximum and the whole sum. (A half that alone is
+          // low, or has little, asks in vain.)
+          const bool low = kF8 && mt < m_run - Sh::kDrop && l_run < 0.5f * need;
+          if (named_sync_or(kMathBar, 128, j == 0 || low || mt > m_run + Sh::kSlack)) {
             mt = fmaxf(mt, misc->mx[sb][half ^ 1][h]);
             if (j == 0) {
               m_run = mt;
             } else {
+              float to = m_run;
               if (mt > m_run + Sh::kSlack) {
-                alpha = exp2f(m_run - mt);
-                m_run = mt;
+                to = mt;
+              } else if (kF8 && mt < m_run - Sh::kDrop && l_run + misc->sum[sb][half ^ 1][h] < need) {
+                to = fmaxf(mt, m_run - Sh::kFar);
+              }
+              if (to != m_run) {
+                alpha = exp2f(m_run - to);
+                m_run = to;
               }
               // O holds the tiles before: every thread scales its head's by alpha (1 for a
-              // head whose maximum stayed).
+              // head whose reference stayed).
               wait_pv(tt - 1);
               tc_fence_after();
               if (ok && __any_sync(0xFFFFFFFFu, alpha != 1.f)) {
