@@ -505,8 +505,8 @@ __global__ void __launch_bounds__(Shape<FMT>::kThreads, 1)
 #pragma unroll
             for (int s = 0; s < Sh::kSubs; ++s) {
               r[s] = rows_at<kRows>(a, p.r, p.off + j, s);
-              // (without rows: a box past the array's end, which reads zeros)
-              if (r[s].rows == 0) r[s].row = a.lat_rows;
+              // (without rows: a box past the end of what lmap covers, which reads zeros)
+              if (r[s].rows == 0) r[s].row = max(a.lat_rows, int64_t{1});
             }
             for (part = 0; part < kParts; ++part) {
               if (tt >= kSlots &&
@@ -1228,7 +1228,7 @@ cudaError_t launch_full_attn(const FullAttnArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   if (a.kv_fmt != DSA_KV_MXFP4) {
     const int elem = a.kv_fmt == DSA_KV_BF16 ? 2 : 1;
-    // (a cache without rows is not read: a map of one row of the queries in its place)
+    // (a cache without rows: a map of one row of the queries, which no box reads)
     const bool any = a.lat_rows > 0;
     e = encode_tma_2d(&lmap, any ? a.latents : a.q, elem, kLatent,
                       any ? static_cast<uint64_t>(a.lat_rows) : 1, kLatent * elem, 128 / elem, kSub);
