@@ -194,7 +194,7 @@ struct Misc {
   float sum[2][2][kHeads];  // (E4M3) the two halves' sums before the tile
   // of a query, by its parity: the output warps may be one behind
   float m_of[2][kHeads], l_of[2][kHeads];
-  float wgt[2][kHeads];    // what a head's O is scaled by
+  float wgt[2][kHeads];    // 1 / the head's sum
   float q_unscale[2][kHeads];  // (E4M3) a head's scores, by the query's parity too
 };
 static_assert(sizeof(Misc) <= kMiscBytes, "misc block");
@@ -944,7 +944,7 @@ __global__ void __launch_bounds__(Shape<FMT>::kThreads, 1)
           l_run += misc->mx[0][0][h];
           misc->m_of[pi][h] = m_run - Sh::kUp;  // what l_run and O are in units of 2^ of
           misc->l_of[pi][h] = l_run;
-          misc->wgt[pi][h] = l_run == 0.f ? 0.f : (kF8 ? a.kv_scale : 1.f) / l_run;
+          misc->wgt[pi][h] = l_run == 0.f ? 0.f : 1.f / l_run;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&misc->stats_full[pi]);
@@ -962,7 +962,8 @@ __global__ void __launch_bounds__(Shape<FMT>::kThreads, 1)
       // half.
       const int slot = 2 * run + (p.off > 0 ? 0 : 1);
       const int ho = (32 * warp + lane) & (kHeads - 1), d0 = dim0 + ((warp >> 1) & 1) * n_cols;
-      const float f = misc->wgt[pi][ho];
+      // (E4M3: the cache's scale on its own, since its quotient by a large sum may be no normal number)
+      const float f = misc->wgt[pi][ho], f2 = kF8 ? a.kv_scale : 1.f;
       if (whole && Sh::kTma) {
         // 64 bytes of each of the warp's heads at a time, over shared memory: the lanes' own stores
         // touch 32 rows each (608 sequences of 64 bf16 rows 26.2 us, this way 22.0).
@@ -979,7 +980,7 @@ __global__ void __launch_bounds__(Shape<FMT>::kThreads, 1)
             uint32_t x[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const __nv_bfloat162 b = __floats2bfloat162_rn(v[8 * k + 2 * e] * f, v[8 * k + 2 * e + 1] * f);
+              const __nv_bfloat162 b = __floats2bfloat162_rn(v[8 * k + 2 * e] * f * f2, v[8 * k + 2 * e + 1] * f * f2);
               x[e] = *reinterpret_cast<const uint32_t*>(&b);
             }
             st_shared_v4(put + ((k ^ put_x) << 4), make_uint4(x[0], x[1], x[2], x[3]));
@@ -1009,7 +1010,7 @@ __global__ void __launch_bounds__(Shape<FMT>::kThreads, 1)
               uint32_t x[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(v[8 * k + 2 * e] * f, v[8 * k + 2 * e + 1] * f);
+                const __nv_bfloat162 b = __floats2bfloat162_rn(v[8 * k + 2 * e] * f * f2, v[8 * k + 2 * e + 1] * f * f2);
                 x[e] = *reinterpret_cast<const uint32_t*>(&b);
               }
               *reinterpret_cast<uint4*>(out + d + 8 * k) = make_uint4(x[0], x[1], x[2], x[3]);
@@ -1190,9 +1191,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps, kJoinPerSm)
         __syncthreads();  // (accs, before the next unit)
       }
       if (n > 0 && (!shared || warp == 0)) {
-        const float s = L == 0.f ? 0.f : (a.kv_fmt == kFmtE4m3 ? a.kv_scale : 1.f) / L;
+        const float s = L == 0.f ? 0.f : 1.f / L, s2 = a.kv_fmt == kFmtE4m3 ? a.kv_scale : 1.f;
         const int64_t row = static_cast<int64_t>(rec.x) * kHeads + h;
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * s, acc.y * s), hi = __floats2bfloat162_rn(acc.z * s, acc.w * s);
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * s * s2, acc.y * s * s2),
+                             hi = __floats2bfloat162_rn(acc.z * s * s2, acc.w * s * s2);
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * kLatent + d) =
             make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
         if (a.lse != nullptr && d == 0) {
