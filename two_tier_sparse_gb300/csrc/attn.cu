@@ -45,7 +45,6 @@
 #include <cstddef>
 
 #include "attn_math.cuh"
-#include "kv_format.cuh"
 
 namespace dsa {
 
@@ -115,6 +114,18 @@ struct Misc {
 static_assert(sizeof(Misc) <= kMiscBytes, "misc block");
 static_assert(offsetof(Misc, inv_l) % 16 == 0 && kMisc % 16 == 0 && kWgt % 16 == 0,
               "16-byte loads of inv_l and of the merge weights");
+
+// 8 E4M3 codes (two words, byte i = code i) -> 8 f16 (exact: every E4M3 value
+// is an f16 normal, subnormal or zero), element i in the low half of word i / 2.
+__device__ __forceinline__ uint4 e4m3x8_to_f16(uint2 c) {
+  uint4 r;
+  asm("{\n .reg .b16 a, b, c, d;\n mov.b32 {a, b}, %4;\n mov.b32 {c, d}, %5;\n"
+      " cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n"
+      " cvt.rn.f16x2.e4m3x2 %2, c;\n cvt.rn.f16x2.e4m3x2 %3, d;\n}\n"
+      : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+      : "r"(c.x), "r"(c.y));
+  return r;
+}
 
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Misc* m,
                                          DeviceStatus* st) {

@@ -512,18 +512,12 @@ template <bool WS, bool F8 = false>
 __device__ __forceinline__ void mma_warp(uint32_t leader, uint32_t d_tmem, uint32_t a_lo,
                                          uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
                                          uint32_t idesc, uint32_t accumulate) {
-  if constexpr (WS && F8) {
+  static_assert(WS || !F8, "8-bit operands: weight-stationary");
+  if constexpr (F8) {
     asm volatile(
         "{\n .reg .pred p, q;\n .reg .b64 x, y;\n setp.ne.b32 q, %0, 0;\n setp.ne.b32 p, %7, 0;\n"
         " mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
         " @q tcgen05.mma.ws.cta_group::1.kind::f8f6f4 [%1], x, y, %6, p;\n}\n" ::"r"(leader),
-        "r"(d_tmem), "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
-        : "memory");
-  } else if constexpr (F8) {
-    asm volatile(
-        "{\n .reg .pred p, q;\n .reg .b64 x, y;\n setp.ne.b32 q, %0, 0;\n setp.ne.b32 p, %7, 0;\n"
-        " mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
-        " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%1], x, y, %6, p;\n}\n" ::"r"(leader),
         "r"(d_tmem), "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
         : "memory");
   } else if constexpr (WS) {

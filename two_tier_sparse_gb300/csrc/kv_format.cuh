@@ -1,5 +1,5 @@
 // Conversions of KV rows to and from the 4-bit cache format (DSA_KV_MXFP4):
-// e2m1 codes under one power-of-two scale per 32 elements (OCP MX v1.0); E4M3 codes to f16.
+// e2m1 codes under one power-of-two scale per 32 elements (OCP MX v1.0).
 #pragma once
 
 #include "kernels.h"
@@ -82,18 +82,6 @@ __device__ __forceinline__ uint4 mx4_decode8(uint32_t c, uint32_t scale2) {
     w[i] = *reinterpret_cast<const uint32_t*>(&p);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// 8 E4M3 codes (two words, byte i = code i) -> 8 f16 (exact: every E4M3 value
-// is an f16 normal, subnormal or zero), element i in the low half of word i / 2.
-__device__ __forceinline__ uint4 e4m3x8_to_f16(uint2 c) {
-  uint4 r;
-  asm("{\n .reg .b16 a, b, c, d;\n mov.b32 {a, b}, %4;\n mov.b32 {c, d}, %5;\n"
-      " cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n"
-      " cvt.rn.f16x2.e4m3x2 %2, c;\n cvt.rn.f16x2.e4m3x2 %3, d;\n}\n"
-      : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-      : "r"(c.x), "r"(c.y));
-  return r;
 }
 
 }  // namespace dsa
