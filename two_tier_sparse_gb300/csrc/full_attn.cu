@@ -1067,8 +1067,10 @@ __device__ __forceinline__ float2 ld_ml(const float2* p) {
 // are few of many parts each, over its CTAs, whose warps share a unit's parts.
 //
 // A call with one split query runs each line of this code once, and fetching it took most of the
-// kernel's 4.7 us. So it is kept short, and each CTA goes through it once without parts
-// while the attention still runs (the kernel is launched ahead and waits for it).
+// kernel's 4.7 us. So it is kept short, and each CTA goes through it once without parts before it waits for
+// the attention: while that still runs, where it leaves SMs idle (1 x 2048). Beside a CTA of the
+// attention there is no room for one of these (4 KB of shared memory are left, and this takes 7), so in a full wave
+// all of the join comes behind it.
 constexpr int kUnits = kHeads * (kLatent / 128);  // of a query
 constexpr int kJoinWarps = 4;
 // A scheduler issues half the time, so what counts are instructions: four loads at once where most queries

@@ -15,13 +15,15 @@
 // 2^-44 by adding 3 (a float's last place there is 2^-22) and reading the bits, which leaves
 // two 32-bit additions where 64-bit ones would bound the pass.
 //
-// One request of 4 drafts and 129280 words takes 5.9 us, a chain of five trips through memory (tokens,
-// their probabilities, the rows, the cluster's total, the place), 64 of 5 drafts 15.2 us, 256 of 4
-// 46.4 us (202 MB, 4.4 TB/s). There a scheduler has seven warps that wait for their loads half the time
-// and issue a third of it (10 instructions a value of the rows). More in flight did not help: a ring in shared memory
-// five iterations deep 52.6 us (20 instructions a value), the next units in registers ahead 49.3,
-// four iterations at once 45.7 (but 9.3 for 7.5 with 512 requests of 5000 words: more code to fetch),
-// CTAs of 128 threads 49.1.
+// One request of 4 drafts and 129280 words takes 5.3 us (replayed from a graph), a chain of five trips
+// through memory (tokens, their probabilities, the rows, the cluster's total, the place), 64 of 5 drafts
+// 13.8, 256 of 4 45.6 (208 MB, one row of a request whose drafts all stand, two of another: 4.6 TB/s), 129 of 3
+// over 50257 bf16 words 10.3 (13 MB). What bounds the large ones are loads in flight: a span is read in
+// rounds of kUnroll iterations a warp, each behind the one before, and a scheduler issues a third of the
+// time. Four iterations a round instead of two take 42.8 for the 256, but 14.3 for the 64, 8.7 for 7.2 with 512 requests of
+// 5000 words (more code to fetch) and 15.4 for 13.7 with 129 of bf16 and two rows; CTAs of 128 threads 45.3, but 17.1 for the
+// 64 and 6.4 for the one. (Of a kernel that took 46.4 for the 256: a ring in shared memory five iterations
+// deep 52.6, the next units in registers ahead 49.3.)
 #include <algorithm>
 #include <type_traits>
 
