@@ -401,8 +401,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         hi[r] = make_uint2(0u, 0u);
         if (arow >= 0) {
           const uint8_t* src = (r0t + r < w_cnt ? swa8 : lat8) + arow * kLatent + lane * 8;
-          lo[r] = __ldg(reinterpret_cast<const uint2*>(src));
-          hi[r] = __ldg(reinterpret_cast<const uint2*>(src + 256));
+          lo[r] = ld_ordered(reinterpret_cast<const uint2*>(src));
+          hi[r] = ld_ordered(reinterpret_cast<const uint2*>(src + 256));
         }
       }
     };

@@ -353,8 +353,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (src != nullptr) {
         const uint4* p = reinterpret_cast<const uint4*>(src);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) code[i] = __ldg(p + g + 4 * i);
-        scales = __ldg(p + kRow4Codes / 16);
+        for (int i = 0; i < 4; ++i) code[i] = ld_ordered(p + g + 4 * i);
+        scales = ld_ordered(p + kRow4Codes / 16);
       }
       ++next;
       return 1;

@@ -626,6 +626,37 @@ __device__ __forceinline__ void tmem_st64(uint32_t taddr, const uint32_t (&v)[64
       : "memory");
 }
 
+// Loads, in the order in which they stand, of what the kernel before this one may write while this
+// one is resident already (behind griddep_wait, this one's or an earlier one's of a step). Read-only
+// loads (__ldg) are for data that nobody writes while the kernel that reads them lives.
+__device__ __forceinline__ uint4 ld_ordered(const uint4* p) {
+  uint4 x;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+               : "l"(p));
+  return x;
+}
+__device__ __forceinline__ uint2 ld_ordered(const uint2* p) {
+  uint2 x;
+  asm volatile("ld.global.v2.u32 {%0, %1}, [%2];\n" : "=r"(x.x), "=r"(x.y) : "l"(p));
+  return x;
+}
+__device__ __forceinline__ float ld_ordered(const float* p) {
+  float x;
+  asm volatile("ld.global.f32 %0, [%1];\n" : "=f"(x) : "l"(p));
+  return x;
+}
+__device__ __forceinline__ float2 ld_ordered(const float2* p) {
+  float2 x;
+  asm volatile("ld.global.v2.f32 {%0, %1}, [%2];\n" : "=f"(x.x), "=f"(x.y) : "l"(p));
+  return x;
+}
+__device__ __forceinline__ int32_t ld_ordered(const int32_t* p) {
+  int32_t x;
+  asm volatile("ld.global.s32 %0, [%1];\n" : "=r"(x) : "l"(p));
+  return x;
+}
+
 // Bits [lo, hi) of the 32-bit word that holds bits [32 k, 32 k + 32).
 __device__ __forceinline__ uint32_t range_bits(int k, int lo, int hi) {
   const int a = max(lo - 32 * k, 0), b = min(hi - 32 * k, 32);

@@ -337,17 +337,6 @@ __device__ __forceinline__ int steps_of(const int (&rows)[2]) {
   return max(1, (rows_end<FMT>(rows) + Shape<FMT>::kStep - 1) / Shape<FMT>::kStep);
 }
 
-// 16 bytes of a row, which the kernel before may write while this one is there already: no read-only
-// load, and in the order in which such loads stand (64 x 8192 116.3 us either way; left to the compiler
-// 117.2, past the first-level cache 124.2).
-__device__ __forceinline__ uint4 ld_row(const uint4* p) {
-  uint4 x;
-  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n"
-               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-               : "l"(p));
-  return x;
-}
-
 template <int FMT>
 __global__ void __launch_bounds__(Shape<FMT>::kThreads, 1)
     full_attn_kernel(const __grid_constant__ FullAttnArgs a, const __grid_constant__ CUtensorMap qmap,
@@ -579,10 +568,12 @@ __global__ void __launch_bounds__(Shape<FMT>::kThreads, 1)
         for (int i = 0; i < kPieces; ++i) code[i] = make_uint4(0u, 0u, 0u, 0u);
         scales = make_uint4(0u, 0u, 0u, 0u);
         if (src != nullptr) {
+          // (64 x 8192 116.3 us as with read-only loads; left to the compiler 117.2, past the first-level
+          // cache 124.2)
           const uint4* p = reinterpret_cast<const uint4*>(src);
 #pragma unroll
-          for (int i = 0; i < kPieces; ++i) code[i] = ld_row(p + g + 4 * i);
-          scales = ld_row(p + kRow4Codes / 16);
+          for (int i = 0; i < kPieces; ++i) code[i] = ld_ordered(p + g + 4 * i);
+          scales = ld_ordered(p + kRow4Codes / 16);
         }
       };
       auto convert = [&](int t, int rows, const uint4 (&code)[kPieces], const uint4& scales) {
@@ -1045,19 +1036,13 @@ __global__ void __launch_bounds__(Shape<FMT>::kThreads, 1)
   }
 }
 
-// Loads of what the attention kernel wrote, behind griddep_wait: not the read-only ones, whose data
-// nobody may write while a kernel that is there already lives, and in the order in which they stand (left to the
-// compiler 1 x 131072 took 50.7 us, read-only 45.3, these 44.5). A part is read once.
+// Four values of a part, which is read once (left to the compiler 1 x 131072 took 50.7 us, with
+// read-only loads 45.3, this way 44.5).
 __device__ __forceinline__ float4 ld_part(const float* p) {
   float4 x;
   asm volatile("ld.global.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];\n"
                : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
                : "l"(p));
-  return x;
-}
-__device__ __forceinline__ float2 ld_ml(const float2* p) {
-  float2 x;
-  asm volatile("ld.global.v2.f32 {%0, %1}, [%2];\n" : "=f"(x.x), "=f"(x.y) : "l"(p));
   return x;
 }
 
@@ -1151,14 +1136,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps, kJoinPerSm)
           // NaN sum does.
 #pragma unroll 1
           for (int k = lane; k < n; k += 32) {
-            const float2 ml = ld_ml(mls + slot_of(k) * kHeads);
+            const float2 ml = ld_ordered(mls + slot_of(k) * kHeads);
             if (!(ml.y == 0.f)) M = fmaxf(M, ml.x);
           }
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(all, M, o));
 #pragma unroll 1
           for (int k = lane; k < n; k += 32) {
-            const float2 ml = ld_ml(mls + slot_of(k) * kHeads);  // (in the L1 by now)
+            const float2 ml = ld_ordered(mls + slot_of(k) * kHeads);  // (in the L1 by now)
             const float w = ml.y == 0.f ? 0.f : ex2_ftz(ml.x - M);
             L = fmaf(w, ml.y, L);
             wgt[k] = w;

@@ -523,7 +523,7 @@ struct QFetch {
 };
 __device__ __forceinline__ uint4 ld_global_v4_early(const void* p) {
   uint4 v;
-  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n"
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
@@ -545,7 +545,7 @@ __device__ __forceinline__ QFetch fetch_query(const ScanArgs& a, int b, int mt) 
   }
   f.w = 0.f;
   if (mt < kIdxHeads) {
-    asm volatile("ld.global.nc.f32 %0, [%1];\n"
+    asm volatile("ld.global.f32 %0, [%1];\n"
                  : "=f"(f.w)
                  : "l"(a.w + static_cast<int64_t>(b) * kIdxHeads + mt));
   }

@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) select_reg_kernel(SelectArgs a) {
 #pragma unroll
     for (int u = 0; u < kBidRegs; ++u) {
       const int i = tid + u * kThreads;
-      bid_r[u] = i < a.k_blocks ? __ldg(bl + i) : -1;
+      bid_r[u] = i < a.k_blocks ? ld_ordered(bl + i) : -1;
     }
   }
   uint32_t key[KPT];
@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) select_reg_kernel(SelectArgs a) {
 #pragma unroll
     for (int j = 0; j < KPT; ++j) {
       const int i = wbase + 32 * j;
-      v[j] = __ldg(sb + (i < n ? i : 0));
+      v[j] = ld_ordered(sb + (i < n ? i : 0));
     }
 #pragma unroll
     for (int j = 0; j < KPT; ++j) key[j] = score_key(wbase + 32 * j < n ? v[j] : -INFINITY);
