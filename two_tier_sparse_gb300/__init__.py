@@ -697,7 +697,7 @@ def _full_cache(cfg, latents, swa, pages: Optional[Pages], B, win_rows):
     if row is None:
         raise DsaError(1, "kv_fmt")
     for name, t in (("latents", latents), ("swa", swa)):
-        if t is not None and (not t.is_contiguous() or t.shape[-1] * t.element_size() != row):
+        if t is not None and (t.dim() == 0 or not t.is_contiguous() or t.shape[-1] * t.element_size() != row):
             raise ValueError(f"{name}: contiguous rows of {row} bytes")
     if swa is not None and tuple(swa.shape[:-1]) != (B, win_rows):
         raise ValueError(f"swa: [{B}, {win_rows}] rows, not {list(swa.shape[:-1])}")
@@ -721,6 +721,8 @@ def full_attn_decode(cfg, q, latents, n_latents, out, ws, swa=None, swa_len=None
                                               None if pages is None else pages._key, lse)
         if code is not None:
             return _check(code, "dsa_full_attn_decode")
+    if q.dim() != 3:
+        raise ValueError(f"q: [B, 64, 512], not {list(q.shape)}")
     B = q.shape[0]
     _bf16("q", q, (B, 64, 512))
     _bf16("out", out, (B, 64, 512))
@@ -756,6 +758,8 @@ def full_attn_multi(cfg, n_tokens, q, latents, out, ws, swa=None, pages: Optiona
                                               None if pages is None else pages._key, lse)
         if code is not None:
             return _check(code, "dsa_full_attn_multi")
+    if q.dim() != 4:
+        raise ValueError(f"q: [B, n_q, 64, 512], not {list(q.shape)}")
     B, n_q = q.shape[0], q.shape[1]
     _bf16("q", q, (B, n_q, 64, 512))
     _bf16("out", out, (B, n_q, 64, 512))
@@ -796,9 +800,10 @@ def verify_drafts(target, draft_tokens, uniform, tokens, n_kept, ws, draft=None,
                                                 tokens, n_kept, n_drop, ws)
         if code is not None:
             return _check(code, "dsa_verify_drafts")
-    B, n = uniform.shape[0], uniform.shape[1] - 1
-    if uniform.dim() != 2 or n < 0 or uniform.dtype != torch.float32 or not uniform.is_contiguous():
+    if uniform.dim() != 2 or uniform.shape[1] < 1 or uniform.dtype != torch.float32 or \
+            not uniform.is_contiguous():
         raise ValueError("uniform: contiguous fp32 [B, n_draft + 1]")
+    B, n = uniform.shape[0], uniform.shape[1] - 1
     p_stride = _prob_rows("target", target, B, n + 1)
     q_stride = 0
     if draft is not None:
