@@ -427,9 +427,10 @@ dsa_status_t dsa_decode_multi(const dsa_config_t* cfg, int n_q, const int32_t* n
  *                order), or both NULL: no window
  *   out:         out, device bf16 [B, 64, 512]; lse: out (optional), device fp32 [B, 64]. A
  *                query without rows gets zeros and -inf.
- * Rows of a page whose table entry is outside the pool are skipped and reported. out and lse
- * overlap no input. B (in dsa_full_attn_multi B * n_q) is at most 2^20, and B * (max_latents / 64
- * + 8) below 2^31 (DSA_ERR_UNSUPPORTED).
+ * Rows of a page whose table entry is outside the pool are skipped and reported. out, lse and
+ * the workspace overlap no input and not one another (DSA_ERR_INVALID_ARG). B (in
+ * dsa_full_attn_multi B * n_q) is at most 2^20, and B * (max_latents / 64 + 8) below 2^31
+ * (DSA_ERR_UNSUPPORTED).
  * The workspace has the size dsa_full_attn_workspace_size gives, the same for
  * every n_queries and format (42 MB: partial outputs of the queries that several SMs share); it is
  * aligned and zeroed like the others, and the calls that need none but a status word
@@ -709,8 +710,9 @@ dsa_status_t dsa_plan_trim(const dsa_config_t* cfg, int B, const int32_t* n_toke
  *   n_kept:       out, device int32 [B]: tokens of the request (k + 1)
  *   n_drop:       out (optional), device int32 [B]: N - k, the drafts that do not stand (what
  *                 dsa_plan_trim takes off a step of N + 1 tokens)
- * Outputs overlap no input and not one another. n_draft is at most DSA_MAX_DRAFTS (0 draws one token from p),
- * vocab at most DSA_MAX_VOCAB, B at most 2^20 (DSA_ERR_UNSUPPORTED). The workspace may be of
+ * Outputs and the status word overlap no input and not one another (DSA_ERR_INVALID_ARG). n_draft
+ * is at most DSA_MAX_DRAFTS (0 draws one token from p), vocab at most DSA_MAX_VOCAB, B at most 2^20
+ * (DSA_ERR_UNSUPPORTED). The workspace may be of
  * any size that dsa_workspace_size gives (its status word is used).
  */
 dsa_status_t dsa_verify_drafts(int B, int n_draft, int64_t vocab, dsa_dtype_t dtype,

@@ -10,6 +10,7 @@
 #include <mutex>
 
 #include "kernels.h"
+#include "kv_format.cuh"
 
 namespace dsa {
 
@@ -995,6 +996,30 @@ dsa_status_t dsa_compress_append(const dsa_config_t* cfg, int B, const int32_t* 
 
 namespace {
 
+// A call's memory: whether something that it writes overlaps something that it reads or
+// writes as well (null: not given).
+struct Bytes {
+  const void* p;
+  int64_t n;
+};
+bool overlap(const Bytes& a, const Bytes& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p != nullptr && b.p != nullptr && a.n > 0 && b.n > 0 &&
+         (x < y ? y - x < static_cast<uint64_t>(a.n) : x - y < static_cast<uint64_t>(b.n));
+}
+template <size_t W, size_t R>
+bool writes_overlap(const Bytes (&written)[W], const Bytes (&read)[R]) {
+  for (size_t i = 0; i < W; ++i) {
+    for (size_t k = i + 1; k < W; ++k) {
+      if (overlap(written[i], written[k])) return true;
+    }
+    for (const Bytes& r : read) {
+      if (overlap(written[i], r)) return true;
+    }
+  }
+  return false;
+}
+
 // Workspace of the attention over whole caches.
 struct FullLayout {
   size_t records, part_ml, parts, total;
@@ -1046,6 +1071,18 @@ dsa_status_t full_attn(const dsa_config_t* cfg, int n_q, const int32_t* lengths,
   if (workspace == nullptr || workspace_bytes < L.total) return DSA_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(workspace) % kAlign) return DSA_ERR_MISALIGNED;
   if (B == 0) return DSA_OK;
+  const int64_t swa_rows = cfg->window + std::max(n_q - 1, 0);
+  const int64_t row = kv_row_bytes(cfg->kv_fmt);
+  const int64_t qo = n * kHeads * kLatent * 2;
+  const Bytes written[] = {{out, qo}, {lse, n * kHeads * 4}, {workspace, static_cast<int64_t>(L.total)}};
+  const Bytes read[] = {{q, qo},
+                        {latents, max_latents > 0 ? rows * row : 0},
+                        {swa, B * swa_rows * row},
+                        {lengths, int64_t{B} * 4},
+                        {swa_len, int64_t{B} * 4},
+                        {pages != nullptr ? pages->page_table : nullptr,
+                         pages != nullptr ? int64_t{B} * pages->pages_per_seq * 4 : 0}};
+  if (writes_overlap(written, read)) return DSA_ERR_INVALID_ARG;
   FullAttnArgs a{};
   a.q = q;
   a.latents = latents;
@@ -1059,7 +1096,7 @@ dsa_status_t full_attn(const dsa_config_t* cfg, int n_q, const int32_t* lengths,
   a.swa = swa;
   a.swa_len = swa_len;
   a.window = cfg->window;
-  a.swa_seq_rows = cfg->window + std::max(n_q - 1, 0);
+  a.swa_seq_rows = swa_rows;
   a.n_queries = static_cast<int>(n);
   a.scale_log2 = tau(*cfg) * 1.4426950408889634f;
   a.kv_fmt = cfg->kv_fmt;
@@ -1239,6 +1276,21 @@ dsa_status_t dsa_verify_drafts(int B, int n_draft, int64_t vocab, dsa_dtype_t dt
   if (workspace == nullptr || workspace_bytes < sizeof(DeviceStatus)) return DSA_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(workspace) % kAlign) return DSA_ERR_MISALIGNED;
   if (B == 0) return DSA_OK;
+  // (CTAs of one request that saw different numbers would not take the same way)
+  const int64_t D = n_draft, size = dtype == DSA_DT_F32 ? 4 : 2;
+  const Bytes written[] = {{tokens, B * (D + 1) * 4},
+                           {n_kept, int64_t{B} * 4},
+                           {n_drop, int64_t{B} * 4},
+                           {workspace, static_cast<int64_t>(sizeof(DeviceStatus))}};
+  auto rows = [&](int64_t n, int64_t stride) {  // bytes from the first row's start to the last one's end
+    return ((n - 1) * std::min(stride, int64_t{1} << 32) + vocab) * size;
+  };
+  const Bytes read[] = {{target, rows(B * (D + 1), target_stride)},
+                        {draft, D > 0 ? rows(B * D, draft_stride) : 0},
+                        {draft_tokens, B * D * 4},
+                        {n_drafts, int64_t{B} * 4},
+                        {uniform, B * (D + 1) * 4}};
+  if (writes_overlap(written, read)) return DSA_ERR_INVALID_ARG;
   VerifyArgs a{};
   a.B = B;
   a.n_draft = n_draft;
