@@ -410,8 +410,8 @@ dsa_status_t dsa_decode_multi(const dsa_config_t* cfg, int n_q, const int32_t* n
  * Attention over the whole cache: every latent of the sequence instead of a selection, and
  * the window rows, under one softmax (miles.radixark.com "DeepSeek-V4.1 Flash", §1: the
  * latent is key and value for all 64 heads). For caches of at most k_tokens latents it is what
- * the sparse calls compute; it serves layers that retrieve nothing, and measures
- * what a selection leaves out. The rows of query b are
+ * the sparse calls compute; over longer ones it measures what a selection leaves out. The rows
+ * of query b are
  *     KV = latents of sequence b, 0 .. n_latents[b] - 1, then swa[b][0 .. swa_len[b] - 1],
  * and out and lse are those of dsa_sparse_attn_decode.
  *   q:           device bf16 [B, 64, 512]
@@ -448,7 +448,7 @@ dsa_status_t dsa_full_attn_decode(const dsa_config_t* cfg, const void* q, const 
  * tokens is verified in one pass: positions, causality and the window rows are those of
  * dsa_decode_multi (query i of sequence b at P = n_tokens[b] - n_q + i sees
  * floor((P + 1) / ratio) latents and its own window), over a contiguous or paged cache of any
- * format.
+ * format. Each query reads its rows anew: this is for a few, not for prompts.
  *   n_tokens: device int32 [B], each >= n_q (the queries of a shorter sequence that have
  *             no position get no rows, reported as DSA_ERR_DEVICE_CHECK); with at most
  *             max_latents latents each (reported; the first max_latents are used)
